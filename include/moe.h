@@ -266,6 +266,141 @@ MOE_API moe_status_t moe_ffn_forward_noalloc(const void* x, const void* router,
                                              float* router_logits, void* stream);
 
 /*
+ * The layer in 8 bits.
+ *
+ * Block format: e4m3 values (one byte each, OCP E4M3 without infinities) with
+ * one fp32 scale per block, value = q * scale.  Rows (activations) have one
+ * scale per 128 consecutive columns: (rows, ceil(cols / 128)).  Weights have
+ * one per 128 x 128 block: (ceil(rows / 128), ceil(cols / 128)) per matrix;
+ * ragged last blocks are shorter.  The gate and the up half of a gate_up
+ * weight (E, 2F, D) are blocked apart: its scales are
+ * (E, 2, ceil(F / 128), ceil(D / 128)).  Any finite scales may be given; the
+ * functions that write the format use max(|v|, 2^-100) / 448 and round to
+ * nearest even.  A NaN stays a NaN; every value of a block that holds an
+ * infinity reads back as NaN.
+ *
+ * All calls below work like moe_ffn_forward: 16-byte aligned device pointers
+ * (offsets: 4 bytes) on the current device, contiguous rows, asynchronous on
+ * `stream`, arguments checked on the host before any launch, no device
+ * memory allocated, no float atomics (results are bitwise repeatable), and
+ * recordable into a CUDA graph after one call outside capture.
+ */
+
+/*
+ * Root-mean-square norm with the residual's addition and an 8-bit output:
+ *
+ *   h = round_dt(x + residual)                 (h = x without a residual)
+ *   y = h / sqrt(mean(h^2) + eps) * weight     (fp32)
+ *   sum_out = h;  out = round_dt(y);  (out_fp8, scales) = blocks of y's rows
+ *
+ *   x, residual, sum_out, out (T, D) dt; weight (D) dt; out_fp8 (T, D) e4m3;
+ *   scales (T, ceil(D / 128)) f32.
+ *
+ * residual, sum_out, out, and the pair out_fp8 and scales may be NULL; one of
+ * out and out_fp8 is required.  sum_out and out may be x or residual
+ * themselves (in place), but not each other; no other overlap is allowed.
+ * Any D up to MOE_NORM_MAX_D (vector loads when D is a multiple of 8).
+ */
+#define MOE_NORM_MAX_D 32768
+MOE_API moe_status_t moe_add_rmsnorm(const void* x, const void* residual, const void* weight,
+                                     float eps, int64_t T, int64_t D, moe_dtype_t dt, void* sum_out,
+                                     void* out, void* out_fp8, float* scales, void* stream);
+
+/*
+ * Blocks of x (matrices, rows, cols), contiguous: block_rows 1 (rows) or 128
+ * (weights).  A gate_up weight (E, 2F, D) is 2E matrices of F rows.
+ */
+MOE_API moe_status_t moe_quantize_fp8(const void* x, moe_dtype_t dt, int64_t matrices, int64_t rows,
+                                      int64_t cols, int block_rows, void* out_fp8, float* scales,
+                                      void* stream);
+
+/*
+ * Routing with groups, from logits (T, E) f32:
+ *
+ *   s = softmax(logits) over the E experts, or sigmoid(logits)
+ *   c = s + selection_bias (without a bias: the logits, which order alike)
+ *   groups: experts [g E/groups, (g+1) E/groups); a group's score is its
+ *       largest c (MOE_GROUP_MAX) or the sum of its two largest s + bias
+ *       (MOE_GROUP_TOP2; the largest alone where a group is one expert); the
+ *       top_groups best groups are kept, equal scores to the lower group
+ *   selected_experts = the K largest c among the kept groups, descending,
+ *       equal ones to the lower expert; K <= top_groups * E / groups
+ *   routing_weights = s_sel / (sum s_sel + 1e-9) with norm_topk_prob, else
+ *       s_sel; times scale (0 counts as 1, so zeroed options are the default)
+ *
+ * The choice is that of scores computed in 64 bits.  A NaN counts as -inf, a
+ * +inf as the largest finite value.  An expert whose c is -inf (a logit that
+ * is masked, a bias of -inf) is chosen after all others of the kept groups,
+ * and a softmax row without a finite logit has scores 0.  groups = 0 is one
+ * group, top_groups = 0 all groups, opts NULL all defaults.
+ */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
+
+typedef struct moe_group_opts {
+  moe_score_t score;
+  const float* selection_bias;   /* (E) f32 device pointer or NULL */
+  int groups;
+  int top_groups;
+  moe_group_score_t group_score;
+  float scale;
+} moe_group_opts_t;
+
+MOE_API moe_status_t moe_select_experts(const float* logits, int64_t T, int E, int K,
+                                        int norm_topk_prob, const moe_group_opts_t* opts,
+                                        int64_t* selected_experts, float* routing_weights,
+                                        void* stream);
+
+/* The same from x (T, D) and the router (E, D), as moe_route takes them;
+ * router_logits (T, E) is required and written. */
+MOE_API moe_status_t moe_route_groups(const void* x, const void* router, const float* router_bias,
+                                      int64_t T, int64_t D, int E, int K, int norm_topk_prob,
+                                      moe_dtype_t dt, const moe_group_opts_t* opts,
+                                      float* router_logits, int64_t* selected_experts,
+                                      float* routing_weights, void* stream);
+
+/*
+ * Block-scaled product, per expert:  out[i, :] = A[i, :] W[e]^T for the rows
+ * i in [offsets[e], offsets[e + 1]) of expert e.
+ *
+ *   a (M, K) e4m3, a_scales (M, ceil(K / 128)); w (E, N, K) e4m3, w_scales
+ *   (E, ceil(N / 128), ceil(K / 128)); offsets (E + 1) int32 device pointer,
+ *   not descending and within [0, M] (others are clamped to that), or NULL
+ *   for E = 1: all M rows; out (M, N) in out_dt (MOE_BF16 or MOE_F32),
+ *   written once per element.  Rows outside [offsets[0], offsets[E]) are
+ *   left as they were.
+ *
+ * Blocks of 128 columns are accumulated in fp32 by the tensor cores, their
+ * scaled sums in fp32, rounded once.  K must be a multiple of 16, N of 8.
+ */
+MOE_API moe_status_t moe_gemm_fp8(const void* a, const float* a_scales, const void* w,
+                                  const float* w_scales, const int* offsets, int E, int64_t M,
+                                  int64_t N, int64_t K, void* out, moe_dtype_t out_dt, void* stream);
+
+/*
+ * The SiLU-gated experts of one layer in 8 bits, for a given routing:
+ *
+ *   h_e = blocks(silu(gate_e x) * up_e x);  y_e = down_e h_e
+ *   out[t, :] = sum_k routing_weights[t, k] * y_{selected_experts[t, k]}(x[t])
+ *
+ *   x_fp8 (T, D), x_scales (T, ceil(D / 128)); selected_experts (T, K) int64;
+ *   routing_weights (T, K) f32; gate_up_proj (E, 2F, D), down_proj (E, D, F)
+ *   e4m3 with their block scales; out (T, D) bf16.
+ *
+ * A slot whose index lies outside [0, E) is unused: it adds nothing, and its
+ * weight is not read as a number (padded tokens get a row of zeros).  The
+ * same expert twice in a token counts twice.  The intermediate is rounded to
+ * 8 bits once, each expert's output to bf16 once, the weighted sum (fp32, in
+ * slot order) to bf16 once.  D and F must be multiples of 16.  With the stage
+ * profiler on the call is recorded like a forward (no router stage).
+ */
+MOE_API size_t moe_experts_workspace_size_fp8(int64_t T, int64_t D, int64_t F, int E, int K);
+MOE_API moe_status_t moe_experts_forward_fp8(
+    const void* x_fp8, const float* x_scales, const int64_t* selected_experts,
+    const float* routing_weights, const void* gate_up_proj, const float* gate_up_scales,
+    const void* down_proj, const float* down_scales, void* out, int64_t T, int64_t D, int64_t F, int E,
+    int K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Which tensor-core grouped GEMM the bf16 path uses (process-wide setting):
  *   MOE_GEMM_AUTO  - CTA pairs when the average expert has >= 512 routed
  *                    rows (large batches), one CTA per tile otherwise;
@@ -375,7 +510,8 @@ MOE_API moe_status_t moe_device_status(void* stream);
  * host watchdog that wants to know, while kernels may still be running,
  * whether and where a bounded wait has given up.  Bit 0 = a wait timed out;
  * bits 8.. = the site (router / grouped GEMM / CTA-pair GEMM, each as
- * producer, MMA issuer or epilogue, then the test probe).  *word is host
+ * producer, MMA issuer or epilogue, then the test probe, then the 8-bit
+ * GEMM's three roles).  *word is host
  * memory.  Returns MOE_OK, MOE_ERR_INVALID_ARG (word NULL) or MOE_ERR_CUDA.
  */
 MOE_API moe_status_t moe_device_error_peek(unsigned int* word);

@@ -35,6 +35,9 @@ enum : unsigned int {
   SITE_PAIR_MMA = 1u << 15,
   SITE_PAIR_EPILOGUE = 1u << 16,
   SITE_PROBE = 1u << 17,
+  SITE_FP8_PRODUCER = 1u << 18,
+  SITE_FP8_MMA = 1u << 19,
+  SITE_FP8_EPILOGUE = 1u << 20,
 };
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.

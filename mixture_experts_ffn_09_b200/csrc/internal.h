@@ -76,6 +76,10 @@ cudaError_t launch_router_tc(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_permute_scan(const int* blockcounts, int B, int E, int* blockbase,
                                 int* totals, cudaStream_t s);
 
+// Block-count tables up to this many entries (blocks x experts) are scanned
+// inside the scatter kernel: each of its blocks reads the whole table.
+constexpr long long kScatterScansItself = 4096;
+
 // Stable scatter of the (token, slot) pairs into expert order: perm[row] =
 // slot, pos[slot] = row; block 0 also writes offsets (E + 1).
 // Slots whose in-block rank reaches the (clamped) block count, and slots
@@ -149,6 +153,77 @@ cudaError_t launch_small_layer_f32(const float* x, const float* router, const fl
                                    const float* b2, int T, int D, int F, int E, int K, int norm,
                                    int gated, float* out, int64_t* sel64, float* wout,
                                    float* logits, int cluster, cudaStream_t s);
+
+// ---- the 8-bit path (block format: fp8.cuh)
+
+// h = x (+ residual), rounded to dt; y = rms norm of h times weight.  Writes
+// sum_out = h, out = y and the blocks (q, scales) of y; each may be null.
+constexpr int kNormMaxD = 32768;
+cudaError_t launch_add_rmsnorm(const void* x, const void* residual, const void* weight, float eps,
+                               int64_t T, int D, int dt, void* sum_out, void* out, uint8_t* q,
+                               float* scales, cudaStream_t s);
+
+// Blocks of `matrices` x (rows, cols): block_rows 1 (a scale per row and 128
+// columns) or 128 (a scale per 128 x 128 block).
+cudaError_t launch_quantize_fp8(const void* x, int dt, int64_t matrices, int64_t rows, int cols,
+                                int block_rows, uint8_t* q, float* scales, cudaStream_t s);
+
+struct SelectArgs {
+  const float* logits;     // (T, E)
+  const float* bias;       // (E) or null
+  int64_t T;
+  int E, K, norm;
+  int score;               // 0 softmax, 1 sigmoid
+  int groups, top_groups;
+  int group_score;         // 0 largest, 1 sum of the two largest
+  float scale;
+  int64_t* selected;       // (T, K)
+  float* weights;          // (T, K)
+};
+cudaError_t launch_select_experts(const SelectArgs& a, cudaStream_t s);
+
+// The block-scaled grouped GEMM.  With q_scales set it is the gated form:
+// the weights hold N gate rows, then N up rows per expert, and out gets the
+// e4m3 blocks of silu(gate) * up.  With perm set the row of A's scales is
+// perm[row] / slots, and with gather that of A itself too.
+struct GemmFp8Args {
+  const void* a;           // (a_rows, K) e4m3
+  const float* a_scales;   // (rows, ceil(K / 128))
+  const void* w;           // (E, N or 2N, K) e4m3
+  const float* w_scales;
+  const int* offsets;      // (E + 1) or null (E = 1, all M rows)
+  const int* perm;
+  int slots;
+  bool gather;
+  int a_rows, M, E, N, K;
+  void* out;
+  bool out_f32;
+  float* q_scales;
+  unsigned int* err;
+};
+cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s);
+
+// 32-token histograms and 32-bit copy of a given selection; an index outside
+// [0, E) becomes E (an unused slot).
+cudaError_t launch_count_selected(const int64_t* selected, int T, int K, int E, int* idx32,
+                                  int* blockcounts, cudaStream_t s);
+
+// Of moe_api.cu: the error of this host thread, the checks and words of the
+// current device, debug-sync mode and the stage profiler.
+moe_status_t fail_status(moe_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+moe_status_t device_ready(unsigned int** err);
+bool debug_sync_passed(cudaStream_t s, const char* stage);   // false: the error is set
+class StageScope {             // one forward's stage timing (off unless profiling)
+ public:
+  explicit StageScope(cudaStream_t s);
+  void begin();
+  void end(int stage);
+
+ private:
+  bool on_;
+  cudaStream_t s_;
+  cudaEvent_t start_ = nullptr;
+};
 
 int num_sms();
 unsigned long long kernel_launches();   // accepted launches so far (note_launch)

@@ -32,9 +32,6 @@ std::atomic<int> g_small_cluster{MOE_SMALL_CLUSTER_AUTO};
 std::atomic<int> g_fused_gather{MOE_FUSED_GATHER_AUTO};
 std::atomic<int> g_pdl{0};   // programmatic dependent launch: opt-in
 std::atomic<int> g_debug_sync_ms{0};   // > 0: bounded wait after every kernel of a forward
-// Block-count tables up to this many entries (blocks x experts) are scanned
-// inside the scatter kernel: each of its blocks reads the whole table.
-constexpr long long kScatterScansItself = 4096;
 
 // The tensor-core GEMM for one launch: CTA pairs pay off when experts have
 // enough rows to fill 256-row tiles.  With gather_perm the A rows are read
@@ -592,7 +589,7 @@ moe_status_t ffn_forward_impl(const void* x, const void* router, const void* gat
       if (!debug_wait(dev, s, "capacity clamp")) return cudaErrorTimeout;
     }
     // a small block-count table is scanned by the scatter blocks themselves
-    const bool own_scan = static_cast<long long>(L.B) * E <= kScatterScansItself;
+    const bool own_scan = static_cast<long long>(L.B) * E <= moe::kScatterScansItself;
     if (!own_scan) {
       r = moe::launch_permute_scan(bcount, L.B, E, bbase, totals, s);
       if (r != cudaSuccess) return r;
@@ -668,7 +665,8 @@ const char* moe_error_sites(unsigned int word) {
   static const char* const kNames[] = {"router producer", "router mma", "router epilogue",
                                        "gemm producer", "gemm mma", "gemm epilogue",
                                        "pair gemm producer", "pair gemm mma",
-                                       "pair gemm epilogue", "bounded-wait probe"};
+                                       "pair gemm epilogue", "bounded-wait probe",
+                                       "fp8 gemm producer", "fp8 gemm mma", "fp8 gemm epilogue"};
   thread_local std::string out;
   out.clear();
   for (int b = 0; b < static_cast<int>(sizeof(kNames) / sizeof(kNames[0])); ++b)
@@ -761,4 +759,53 @@ int num_sms() {
 
 namespace moe {
 void set_last_error(const char* msg) { g_last_error = msg ? msg : ""; }
+
+moe_status_t fail_status(moe_status_t st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return st;
+}
+
+moe_status_t device_ready(unsigned int** err) {
+  DevInfo* dev = nullptr;
+  const moe_status_t st = device_info(&dev);
+  if (st == MOE_OK) *err = dev->err;
+  return st;
+}
+
+bool debug_sync_passed(cudaStream_t s, const char* stage) {
+  if (g_debug_sync_ms.load() <= 0) return true;
+  DevInfo* dev = nullptr;
+  return device_info(&dev) == MOE_OK && debug_wait(dev, s, stage);
+}
+
+StageScope::StageScope(cudaStream_t s) : s_(s) {
+  std::lock_guard<std::mutex> lock(g_prof_mu);
+  on_ = g_prof.enabled;
+  if (on_) g_prof.calls++;
+}
+
+void StageScope::begin() {
+  if (!on_) return;
+  {
+    std::lock_guard<std::mutex> lock(g_prof_mu);
+    start_ = prof_event();
+  }
+  if (start_) cudaEventRecord(start_, s_);
+}
+
+void StageScope::end(int stage) {
+  if (!on_) return;
+  cudaEvent_t b = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(g_prof_mu);
+    b = prof_event();
+    if (start_ && b) g_prof.recs.push_back({stage, {start_, b}});
+  }
+  if (b) cudaEventRecord(b, s_);
+}
 }  // namespace moe

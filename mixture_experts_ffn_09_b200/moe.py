@@ -9,12 +9,15 @@ The functions keep the C names without the ``moe_`` prefix:
 * :func:`ffn_forward`   - moe_ffn_forward (router, permutation, grouped GEMMs,
   combine), on caller-provided torch tensors;
 * :func:`route`         - moe_route (router only);
+* :func:`add_rmsnorm`, :func:`quantize_fp8`, :func:`select_experts`,
+  :func:`route_groups`, :func:`gemm_fp8`, :func:`experts_forward_fp8`,
+  :func:`experts_workspace_size_fp8` - the layer in 8 bits;
 * :func:`workspace_size`, :func:`device_status`, :func:`profile_enable`,
   :func:`profile_read`, :func:`status_string`, :func:`abi_version`.
 
 :class:`MoEBlock` mirrors the interface of mojolearn.MoEBlock (forward,
 load_state_dict, router_logits_, selected_experts_, routing_weights_) on
-top of these calls.
+top of these calls; :class:`MoEBlockFP8` is the block in 8 bits.
 """
 from __future__ import annotations
 
@@ -47,6 +50,10 @@ NUM_STAGES = 6
 
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
+GROUP_MAX = 0
+GROUP_TOP2 = 1
+GROUP_NAMES = {"max": GROUP_MAX, "top2": GROUP_TOP2}
+QUANT_BLOCK = 128
 SCORE_NAMES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 
 _lock = threading.Lock()
@@ -59,6 +66,13 @@ class RouteOpts(ctypes.Structure):
                 ("dynamic_threshold", ctypes.c_float), ("capacity_factor", ctypes.c_float),
                 ("seq_len", ctypes.c_int64), ("slot_kept", ctypes.c_void_p),
                 ("balance", ctypes.c_void_p)]
+
+
+class GroupOpts(ctypes.Structure):
+    """moe_group_opts_t (include/moe.h)."""
+    _fields_ = [("score", ctypes.c_int), ("selection_bias", ctypes.c_void_p),
+                ("groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class MoEError(RuntimeError):
@@ -95,6 +109,23 @@ def lib() -> ctypes.CDLL:
         L.moe_route_ex.restype = i32
         L.moe_route.argtypes = [vp, vp, vp, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp]
         L.moe_route.restype = i32
+        f32 = ctypes.c_float
+        L.moe_add_rmsnorm.argtypes = [vp, vp, vp, f32, i64, i64, i32, vp, vp, vp, vp, vp]
+        L.moe_add_rmsnorm.restype = i32
+        L.moe_quantize_fp8.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp]
+        L.moe_quantize_fp8.restype = i32
+        L.moe_select_experts.argtypes = [vp, i64, i32, i32, i32, ctypes.POINTER(GroupOpts), vp, vp, vp]
+        L.moe_select_experts.restype = i32
+        L.moe_route_groups.argtypes = [vp, vp, vp, i64, i64, i32, i32, i32, i32,
+                                       ctypes.POINTER(GroupOpts), vp, vp, vp, vp]
+        L.moe_route_groups.restype = i32
+        L.moe_gemm_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, i32, vp]
+        L.moe_gemm_fp8.restype = i32
+        L.moe_experts_workspace_size_fp8.argtypes = [i64, i64, i64, i32, i32]
+        L.moe_experts_workspace_size_fp8.restype = sz
+        L.moe_experts_forward_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32,
+                                              i32, vp, sz, vp]
+        L.moe_experts_forward_fp8.restype = i32
         L.moe_status_string.argtypes = [i32]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_last_error.argtypes = []
@@ -378,6 +409,165 @@ def route(x, router, K: int, norm_topk_prob: bool, selected_experts, routing_wei
     _check(st)
 
 
+def _blocks(n: int) -> int:
+    return -(-n // QUANT_BLOCK)
+
+
+def _rows(t) -> int:
+    return int(t.numel() // t.shape[-1]) if t.shape[-1] else 0
+
+
+def add_rmsnorm(x, weight, eps: float, residual=None, sum_out=None, out=None, out8=None,
+                scales=None, stream=None) -> None:
+    """moe_add_rmsnorm on torch tensors.  x (..., D); weight (D,); residual,
+    sum_out, out like x; out8 float8_e4m3fn like x; scales float32
+    (rows, ceil(D / 128))."""
+    import torch
+    D = int(x.shape[-1])
+    T = _rows(x)
+    dt = _dtype_code(x)
+    if dt in (F32, BF16) and T > 0:
+        _expect(x, x.shape, "x")
+        _expect(weight, (D,), "weight", x.dtype)
+        _expect(residual, x.shape, "residual", x.dtype, False)
+        _expect(sum_out, x.shape, "sum_out", x.dtype, False)
+        _expect(out, x.shape, "out", x.dtype, False)
+        _expect(out8, x.shape, "out8", torch.float8_e4m3fn, False)
+        _expect(scales, (T, _blocks(D)), "scales", torch.float32, False)
+    _check(lib().moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), T, D, dt,
+                                 _ptr(sum_out), _ptr(out), _ptr(out8), _ptr(scales),
+                                 _stream(stream)))
+
+
+def quantize_fp8(x, out8, scales, block_rows: int = 1, stream=None) -> None:
+    """moe_quantize_fp8 on torch tensors.  x (..., rows, cols), out8
+    float8_e4m3fn like x, scales float32: (..., rows, ceil(cols / 128)) with
+    block_rows 1, (..., ceil(rows / 128), ceil(cols / 128)) with 128.  Give a
+    gate_up weight (E, 2F, D) as its view (E, 2, F, D)."""
+    import torch
+    if x.dim() < 2:
+        raise ValueError("x needs at least two dimensions (rows, cols)")
+    rows, cols = int(x.shape[-2]), int(x.shape[-1])
+    dt = _dtype_code(x)
+    if dt in (F32, BF16) and x.numel() > 0 and block_rows in (1, QUANT_BLOCK):
+        _expect(x, x.shape, "x")
+        _expect(out8, x.shape, "out8", torch.float8_e4m3fn)
+        _expect(scales, (*x.shape[:-2], rows if block_rows == 1 else _blocks(rows), _blocks(cols)),
+                "scales", torch.float32)
+    mats = x.numel() // (rows * cols) if rows * cols else 0
+    _check(lib().moe_quantize_fp8(_ptr(x), dt, mats, rows, cols, int(block_rows), _ptr(out8),
+                                  _ptr(scales), _stream(stream)))
+
+
+def _group_opts(score, selection_bias, groups, top_groups, group_score, scale) -> GroupOpts:
+    sc = SCORE_NAMES.get(score, 99) if isinstance(score, str) else int(score)
+    gs = GROUP_NAMES.get(group_score, 99) if isinstance(group_score, str) else int(group_score)
+    return GroupOpts(sc, _ptr(selection_bias), int(groups), int(top_groups), gs, float(scale))
+
+
+def select_experts(logits, K: int, norm_topk_prob: bool, selected_experts, routing_weights,
+                   score="softmax", selection_bias=None, groups: int = 1, top_groups: int = 0,
+                   group_score="max", scale: float = 1.0, stream=None) -> None:
+    """moe_select_experts on torch tensors: logits (..., E) float32,
+    selected_experts int64 and routing_weights float32 of K per row."""
+    import torch
+    E = int(logits.shape[-1])
+    T = _rows(logits)
+    if T > 0 and K >= 1:
+        _expect(logits, logits.shape, "logits", torch.float32)
+        _expect(selected_experts, (T, K), "selected_experts", torch.int64)
+        _expect(routing_weights, (T, K), "routing_weights", torch.float32)
+        _expect(selection_bias, (E,), "selection_bias", torch.float32, False)
+    o = _group_opts(score, selection_bias, groups, top_groups, group_score, scale)
+    _check(lib().moe_select_experts(_ptr(logits), T, E, K, 1 if norm_topk_prob else 0,
+                                    ctypes.byref(o), _ptr(selected_experts), _ptr(routing_weights),
+                                    _stream(stream)))
+
+
+def route_groups(x, router, K: int, norm_topk_prob: bool, router_logits, selected_experts,
+                 routing_weights, router_bias=None, score="softmax", selection_bias=None,
+                 groups: int = 1, top_groups: int = 0, group_score="max", scale: float = 1.0,
+                 stream=None) -> None:
+    """moe_route_groups on torch tensors: the router's product, then
+    :func:`select_experts`; router_logits (T, E) float32 is written."""
+    import torch
+    D = int(x.shape[-1])
+    T = _rows(x)
+    E = int(router.shape[0])
+    dt = _dtype_code(x)
+    if dt in (F32, BF16) and T > 0 and K >= 1:
+        _expect(x, x.shape, "x")
+        _expect(router, (E, D), "router", x.dtype)
+        _expect(router_bias, (E,), "router_bias", torch.float32, False)
+        _expect(router_logits, (T, E), "router_logits", torch.float32)
+        _expect(selected_experts, (T, K), "selected_experts", torch.int64)
+        _expect(routing_weights, (T, K), "routing_weights", torch.float32)
+        _expect(selection_bias, (E,), "selection_bias", torch.float32, False)
+    o = _group_opts(score, selection_bias, groups, top_groups, group_score, scale)
+    _check(lib().moe_route_groups(_ptr(x), _ptr(router), _ptr(router_bias), T, D, E, K,
+                                  1 if norm_topk_prob else 0, dt, ctypes.byref(o),
+                                  _ptr(router_logits), _ptr(selected_experts),
+                                  _ptr(routing_weights), _stream(stream)))
+
+
+def gemm_fp8(a, a_scales, w, w_scales, out, offsets=None, stream=None) -> None:
+    """moe_gemm_fp8 on torch tensors: a (M, K), w (E, N, K) or (N, K)
+    float8_e4m3fn; scales float32; offsets (E + 1,) int32; out (M, N)
+    bfloat16 or float32."""
+    import torch
+    if a.dim() != 2 or w.dim() not in (2, 3):
+        raise ValueError("a must be (M, K), w (E, N, K) or (N, K)")
+    M, K = int(a.shape[0]), int(a.shape[1])
+    N = int(w.shape[-2])
+    E = int(w.shape[0]) if w.dim() == 3 else 1
+    dt = _dtype_code(out)
+    if dt in (F32, BF16) and M > 0 and N > 0 and K > 0 and E > 0:
+        f8 = torch.float8_e4m3fn
+        _expect(a, a.shape, "a", f8)
+        _expect(a_scales, (M, _blocks(K)), "a_scales", torch.float32)
+        _expect(w, (*w.shape[:-1], K), "w", f8)
+        _expect(w_scales, (*w.shape[:-2], _blocks(N), _blocks(K)), "w_scales", torch.float32)
+        _expect(offsets, (E + 1,), "offsets", torch.int32, False)
+        _expect(out, (M, N), "out")
+    _check(lib().moe_gemm_fp8(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), E, M,
+                              N, K, _ptr(out), dt, _stream(stream)))
+
+
+def experts_workspace_size_fp8(T: int, D: int, F: int, E: int, K: int) -> int:
+    return int(lib().moe_experts_workspace_size_fp8(T, D, F, E, K))
+
+
+def experts_forward_fp8(x, x_scales, selected_experts, routing_weights, gate_up_proj, gate_up_scales,
+                        down_proj, down_scales, out, workspace=None, stream=None) -> None:
+    """moe_experts_forward_fp8 on torch tensors: x (..., D), gate_up_proj
+    (E, 2F, D) and down_proj (E, D, F) float8_e4m3fn; x_scales
+    (T, ceil(D / 128)), gate_up_scales (E, 2, ceil(F / 128), ceil(D / 128)),
+    down_scales (E, ceil(D / 128), ceil(F / 128)) float32; selected_experts
+    (T, K) int64, routing_weights (T, K) float32; out bfloat16 like x."""
+    import torch
+    D = int(x.shape[-1])
+    T = _rows(x)
+    E, F = int(down_proj.shape[0]), int(down_proj.shape[-1])
+    K = int(selected_experts.shape[-1])
+    if T > 0 and E > 0 and F > 0 and K > 0:
+        f8, f32 = torch.float8_e4m3fn, torch.float32
+        db, fb = _blocks(D), _blocks(F)
+        _expect(x, x.shape, "x", f8)
+        _expect(x_scales, (T, db), "x_scales", f32)
+        _expect(selected_experts, (T, K), "selected_experts", torch.int64)
+        _expect(routing_weights, (T, K), "routing_weights", f32)
+        _expect(gate_up_proj, (E, 2 * F, D), "gate_up_proj", f8)
+        _expect(gate_up_scales, (E, 2, fb, db), "gate_up_scales", f32)
+        _expect(down_proj, (E, D, F), "down_proj", f8)
+        _expect(down_scales, (E, db, fb), "down_scales", f32)
+        _expect(out, x.shape, "out", torch.bfloat16)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().moe_experts_forward_fp8(
+        _ptr(x), _ptr(x_scales), _ptr(selected_experts), _ptr(routing_weights), _ptr(gate_up_proj),
+        _ptr(gate_up_scales), _ptr(down_proj), _ptr(down_scales), _ptr(out), T, D, F, E, K,
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
 GEMM_AUTO, GEMM_1SM, GEMM_2SM = 0, 1, 2
 
 
@@ -540,6 +730,79 @@ class MoEBlock:
         ffn_forward(x, self.router, self.gate_up_proj, self.down_proj, E, K, self.norm_topk_prob,
                     self.act, out, self.selected_experts_, self.routing_weights_,
                     self.router_bias, self.b1, self.b2, self.router_logits_, self._ws, stream)
+        return out
+
+    __call__ = forward
+
+
+class MoEBlockFP8:
+    """The SiLU-gated block with 8-bit experts: optional residual RMS norm,
+    routing with groups, experts in the block format (include/moe.h).
+
+    Made from bf16 or float32 weights in the Hugging Face layout, which it
+    quantises once: router (E, D) stays in its type, gate_up_proj (E, 2F, D)
+    and down_proj (E, D, F) become e4m3 with block scales.  With norm_weight
+    (D,) the input is normed first; ``forward(x, residual)`` then returns the
+    block's output, and ``residual_`` holds x + residual.  Routing options are
+    those of :func:`select_experts`.  Keeps ``router_logits_``,
+    ``selected_experts_`` and ``routing_weights_`` of the last call."""
+
+    def __init__(self, router, gate_up_proj, down_proj, top_k: int = 2, norm_topk_prob: bool = True,
+                 norm_weight=None, eps: float = 1e-6, router_bias=None, **routing):
+        import torch
+        E, F2, D = (int(n) for n in gate_up_proj.shape)
+        F = F2 // 2
+        if not 1 <= int(top_k) <= E:
+            raise ValueError(f"top_k={top_k} outside [1, {E}]")
+        if tuple(down_proj.shape) != (E, D, F) or F2 != 2 * F:
+            raise ValueError(f"down_proj has shape {tuple(down_proj.shape)}, expected {(E, D, F2 / 2)}")
+        self.router, self.router_bias = router, router_bias
+        self.norm_weight, self.eps = norm_weight, float(eps)
+        self.top_k, self.norm_topk_prob, self.routing = int(top_k), bool(norm_topk_prob), routing
+        new = lambda shape, dt: torch.empty(shape, dtype=dt, device=gate_up_proj.device)  # noqa: E731
+        f8, f32 = torch.float8_e4m3fn, torch.float32
+        self.gate_up_proj, self.down_proj = new((E, 2 * F, D), f8), new((E, D, F), f8)
+        self.gate_up_scales = new((E, 2, _blocks(F), _blocks(D)), f32)
+        self.down_scales = new((E, _blocks(D), _blocks(F)), f32)
+        quantize_fp8(gate_up_proj.view(E, 2, F, D), self.gate_up_proj.view(E, 2, F, D),
+                     self.gate_up_scales, QUANT_BLOCK)
+        quantize_fp8(down_proj, self.down_proj, self.down_scales, QUANT_BLOCK)
+        self._ws = None
+        self.residual_ = self.router_logits_ = self.selected_experts_ = self.routing_weights_ = None
+
+    @property
+    def num_experts(self) -> int:
+        return int(self.router.shape[0])
+
+    def forward(self, x, residual=None, stream=None):
+        import torch
+        if residual is not None and self.norm_weight is None:
+            raise ValueError("a residual needs norm_weight")
+        E, F, D = int(self.down_proj.shape[0]), int(self.down_proj.shape[-1]), int(x.shape[-1])
+        T, K = _rows(x), self.top_k
+        new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
+        x8, xs = new(x.shape, torch.float8_e4m3fn), new((T, _blocks(D)), torch.float32)
+        if self.norm_weight is not None:
+            self.residual_ = torch.empty_like(x) if residual is not None else x
+            y = torch.empty_like(x)
+            add_rmsnorm(x, self.norm_weight, self.eps, residual,
+                        self.residual_ if residual is not None else None, y, x8, xs, stream)
+            x = y
+        else:
+            quantize_fp8(x.view(T, D), x8.view(T, D), xs, 1, stream)
+        self.router_logits_ = new((T, E), torch.float32)
+        self.selected_experts_ = new((T, K), torch.int64)
+        self.routing_weights_ = new((T, K), torch.float32)
+        route_groups(x, self.router, K, self.norm_topk_prob, self.router_logits_,
+                     self.selected_experts_, self.routing_weights_, self.router_bias, stream=stream,
+                     **self.routing)
+        need = experts_workspace_size_fp8(T, D, F, E, K)
+        if self._ws is None or self._ws.numel() < need or self._ws.device != x.device:
+            self._ws = new(max(need, 1), torch.uint8)
+        out = new(x.shape, torch.bfloat16)
+        experts_forward_fp8(x8, xs, self.selected_experts_, self.routing_weights_, self.gate_up_proj,
+                            self.gate_up_scales, self.down_proj, self.down_scales, out, self._ws,
+                            stream)
         return out
 
     __call__ = forward

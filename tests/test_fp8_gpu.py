@@ -1,0 +1,449 @@
+"""The 8-bit path on the GPU against float64 (tests/fp8_lib.py)."""
+import pytest
+import torch
+
+import fp8_lib as R
+from mixture_experts_ffn_09_b200 import moe
+
+pytestmark = pytest.mark.gpu
+
+F8 = torch.float8_e4m3fn
+U32 = 2.0 ** -24                       # half a step of fp32
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U32}
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(autouse=True)
+def healthy():
+    yield
+    torch.cuda.synchronize()
+    assert moe.device_status() == moe.MOE_OK
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(*shape, seed=0, std=1.0):
+    return torch.randn(*shape, generator=gen(seed), device="cuda") * std
+
+
+def rows8(M, K, seed):
+    q = (randn(M, K, seed=seed) * 150).clamp(-448, 448).to(F8)
+    return q, torch.exp(randn(M, R.nblk(K), seed=seed + 1) * 0.5) / 150
+
+
+def weight8(E, N, K, seed, std=0.05):
+    q = (randn(E, N, K, seed=seed) * 100).clamp(-448, 448).to(F8)
+    return q, (torch.rand(E, R.nblk(N), R.nblk(K), generator=gen(seed + 1), device="cuda") + 0.5) * std / 100
+
+
+# --------------------------------------------------------------------- norm
+def run_norm(x, r, w, eps, sum_out=True, out=True, quant=True):
+    T, D = x.shape
+    o = dict(sum_out=torch.empty_like(x) if sum_out else None, out=torch.empty_like(x) if out else None,
+             out8=torch.empty(T, D, dtype=F8, device="cuda") if quant else None,
+             scales=torch.empty(T, R.nblk(D), device="cuda") if quant else None)
+    moe.add_rmsnorm(x, w, eps, residual=r, **o)
+    return o
+
+
+def check_norm(x, r, w, eps, o):
+    h, y = R.add_rmsnorm(x, r, w, eps)
+    # mean of squares: at most 32 terms a lane, 10 levels of a tree, halved by the root;
+    # root, quotient and two products: 2 steps each at most
+    rel = (21 + 8) * U32
+    if o["sum_out"] is not None:
+        assert torch.equal(o["sum_out"], h)
+    if o["out"] is not None:
+        err = (o["out"].double() - y).abs()
+        assert (err <= y.abs() * (rel + HALF[x.dtype] * (1 + rel)) + 1e-37).all()
+    if o["out8"] is not None:
+        _, s, half = R.quantize(y)
+        assert ((o["scales"].double() - s).abs() <= s * (rel + 2 * U32)).all()
+        # half a step of e4m3 (a value at the end of a binade may use the next one's step), and the scale's error
+        err = (R.wide(o["out8"], o["scales"]) - y).abs()
+        assert (err <= torch.maximum(half, y.abs() * 2.0 ** -4) * (1 + 1e-4) + y.abs() * (2 * rel + 8 * U32)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,D", [(1, 1), (3, 7), (1, 128), (5, 130), (33, 264), (2, 4096), (7, 2567),
+                                 (1000, 96), (3, 8192), (2, 8200), (2, 16376), (3, 16384), (2, 32768),
+                                 (2, 8193), (2, 16383), (2, 32761)])
+def test_norm(dtype, T, D):
+    x, r = randn(T, D, seed=1).to(dtype), randn(T, D, seed=2, std=3.0).to(dtype)
+    w = (1 + 0.3 * randn(D, seed=3)).to(dtype)
+    check_norm(x, r, w, 1e-6, run_norm(x, r, w, 1e-6))
+    check_norm(x, None, w, 0.5, run_norm(x, None, w, 0.5, sum_out=T % 2 == 0))
+
+
+@pytest.mark.parametrize("out,quant,sum_out", [(True, False, False), (False, True, True), (False, True, False)])
+def test_norm_outputs(out, quant, sum_out):
+    x, r, w = (randn(9, 520, seed=s).bfloat16() for s in (1, 2, 3))
+    w = w[0].contiguous()
+    check_norm(x, r, w, 1e-5, run_norm(x, r, w, 1e-5, sum_out, out, quant))
+
+
+@pytest.mark.parametrize("D", [512, 515])
+def test_norm_in_place_and_repeatable(D):
+    x, r, w = randn(64, D, seed=1).bfloat16(), randn(64, D, seed=2).bfloat16(), randn(D, seed=3).bfloat16()
+    want = run_norm(x, r, w, 1e-6)
+    for _ in range(2):
+        x2, r2 = x.clone(), r.clone()
+        moe.add_rmsnorm(x2, w, 1e-6, residual=r2, sum_out=r2, out=x2)
+        assert torch.equal(r2, want["sum_out"]) and torch.equal(x2, want["out"])
+
+
+@pytest.mark.parametrize("D", [256, 259])
+def test_norm_extremes(D):
+    """Rows of zeros, of huge and tiny values, and non-finite ones that stay in their row."""
+    x = randn(8, D, seed=4)
+    x[0] = 0.0
+    x[1] *= 1e18
+    x[2] *= 1e-30
+    x[3, :128] = 0.0                   # a block of zeros beside others
+    x[4, 5] = NAN
+    x[5, 5] = INF
+    w = torch.ones(D, device="cuda")
+    o = run_norm(x, None, w, 1e-6)
+    fine = [0, 1, 2, 3, 6, 7]
+    check_norm(x[fine], None, w, 1e-6, {k: v[fine] for k, v in o.items()})
+    assert o["out"][4].isnan().all()
+    assert o["out8"][4].float().isnan().all()
+    assert o["out"][5].isnan().sum() == 1 and R.wide(o["out8"], o["scales"])[5, :128].isnan().any()
+    assert (o["out8"][0].float() == 0).all() and (o["scales"] > 0).all()
+
+
+# ----------------------------------------------------------------- quantise
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape,block_rows", [((1, 1), 1), ((5, 300), 1), ((3, 7, 264), 1), ((1, 1), 128),
+                                              ((2, 200, 264), 128), ((3, 2, 130, 77), 128), ((128, 128), 128)])
+def test_quantize(dtype, shape, block_rows):
+    x = (randn(*shape, seed=5) * torch.exp(randn(*shape[:-1], 1, seed=6))).to(dtype)
+    x.view(-1, shape[-1])[0, : min(128, shape[-1])] = 0
+    q = torch.empty(shape, dtype=F8, device="cuda")
+    rows = shape[-2] if block_rows == 1 else R.nblk(shape[-2])
+    s = torch.empty(*shape[:-2], rows, R.nblk(shape[-1]), device="cuda")
+    moe.quantize_fp8(x, q, s, block_rows)
+    v = x.double()
+    _, want, half = R.quantize(v, block_rows)
+    assert ((s.double() - want).abs() <= want * 2 * U32).all()
+    err = (R.wide(q, s, block_rows) - v).abs()
+    assert (err <= torch.maximum(half, v.abs() * 2.0 ** -4) * (1 + 1e-4) + v.abs() * 8 * U32).all()
+
+
+# ------------------------------------------------------------------- select
+def check_select(logits, K, norm, **o):
+    T = logits.shape[0]
+    sel = torch.full((T, K), -7, dtype=torch.int64, device="cuda")
+    w = torch.full((T, K), NAN, device="cuda")
+    moe.select_experts(logits, K, norm, sel, w, **o)
+    want, ww = R.select(logits, K, norm, **o)
+    assert torch.equal(sel, want)
+    # scores: 20 steps (the exponent's rounding, 13 of the sum); the sum of the chosen: 8 more; 3 roundings
+    assert ((w.double() - ww).abs() <= ww.abs() * 40 * U32 + 1e-37).all()
+
+
+OPTS = [dict(), dict(score="sigmoid"), dict(groups=4, top_groups=2), dict(groups=2, top_groups=1, group_score="top2"),
+        dict(score="sigmoid", groups=4, top_groups=3, group_score="top2", scale=2.5)]
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("o", OPTS, ids=str)
+@pytest.mark.parametrize("T,E", [(1, 4), (2, 8), (3, 12), (65, 20), (257, 32), (100, 64), (31, 100), (33, 128),
+                                 (40, 160), (129, 252), (5000, 256)])
+def test_select(T, E, o, bias):
+    l = randn(T, E, seed=E, std=2.0)
+    b = 0.1 * randn(E, seed=9) if bias else None
+    most = E // o.get("groups", 1) * o.get("top_groups", 1)
+    for K in {1, min(8, most), most if T < 100 else 1}:
+        check_select(l, K, K % 2 == 0, selection_bias=b, **o)
+
+
+@pytest.mark.parametrize("E,groups,top", [(6, 3, 2), (15, 5, 2), (252, 63, 10), (256, 256, 9), (256, 16, 3), (256, 32, 5),
+                                          (96, 3, 1), (64, 64, 64)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_select_group_layouts(E, groups, top, score, group_score):
+    o = dict(score=score, groups=groups, top_groups=top, group_score=group_score)
+    l = randn(77, E, seed=E)
+    check_select(l, min(6, top * (E // groups)), True, **o)
+    check_select(l, min(6, top * (E // groups)), False, selection_bias=randn(E, seed=3), **o)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("o", OPTS, ids=str)
+def test_select_near_and_equal_scores(o, bias):
+    """Scores one rounding apart and exactly equal ones: the choice is that of 64 bits, ties to the lower index."""
+    T, E = 600, 64
+    l = randn(T, 1, seed=1) + torch.randint(-3, 4, (T, E), generator=gen(2), device="cuda") * 1e-7
+    l[:200] = torch.randint(-2, 3, (200, E), generator=gen(3), device="cuda").float()
+    l[200:250] = 0.0
+    b = torch.randint(-2, 3, (E,), generator=gen(4), device="cuda") * 3e-8 if bias else None
+    check_select(l, 4, True, selection_bias=b, **o)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("o", OPTS, ids=str)
+def test_select_masked_and_not_finite(o, bias):
+    T, E = 64, 32
+    l = randn(T, E, seed=1)
+    l[torch.rand(T, E, generator=gen(2), device="cuda") < 0.7] = -INF
+    l[0] = -INF                                  # nothing left
+    l[1] = torch.finfo(torch.float32).min
+    l[2, :] = NAN
+    l[3, 5], l[3, 9] = NAN, INF
+    l[4, 31] = 3.0e38
+    b = None
+    if bias:
+        b = 0.1 * randn(E, seed=3)
+        b[::5] = -INF                            # experts switched off
+    check_select(l, 6, True, selection_bias=b, **o)
+    check_select(l, 6, False, selection_bias=b, **o)
+
+
+def test_route_groups():
+    """Both dtypes: the logits are the router's, the choice is that of select_experts on them."""
+    for dtype, T, D, E in ((torch.bfloat16, 300, 264, 64), (torch.float32, 37, 33, 20)):
+        x, r = randn(T, D, seed=1).to(dtype), randn(E, D, seed=2, std=0.1).to(dtype)
+        rb = randn(E, seed=3)
+        o = dict(score="sigmoid", selection_bias=randn(E, seed=4), groups=4, top_groups=2, group_score="top2")
+        lg, lg2 = torch.empty(T, E, device="cuda"), torch.empty(T, E, device="cuda")
+        sel, w = torch.empty(T, 5, dtype=torch.int64, device="cuda"), torch.empty(T, 5, device="cuda")
+        moe.route_groups(x, r, 5, True, lg, sel, w, router_bias=rb, **o)
+        s2, w2 = torch.empty_like(sel), torch.empty_like(w)
+        moe.route(x, r, 5, True, s2, w2, router_bias=rb, router_logits=lg2)
+        assert torch.equal(lg, lg2)
+        want, _ = R.select(lg, 5, True, **o)
+        assert torch.equal(sel, want)
+
+
+# ------------------------------------------------------------------ product
+def check_product(E, M, N, K, offsets, dtype=torch.bfloat16, seed=0):
+    a, sa = rows8(M, K, seed)
+    w, sw = weight8(E, N, K, seed + 10)
+    out = torch.full((M, N), 7.0, dtype=dtype, device="cuda")
+    o = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    moe.gemm_fp8(a, sa, w, sw, out, offsets=o)
+    C, S, live = R.product(a, sa, w, sw, offsets or [0, M])
+    # 128 products a block (one step each if the tensor core truncates), a scaled sum per block, two scale products
+    gamma = (128 + R.nblk(K) + 4) * 2 * U32
+    err = (out.double() - C).abs()
+    assert (err[live] <= (S * gamma + C.abs() * HALF[dtype] * 1.01)[live]).all()
+    assert (out[~live] == 7.0).all()
+    again = torch.full_like(out, 7.0)
+    moe.gemm_fp8(a, sa, w, sw, again, offsets=o)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (1, 256, 128), (7, 136, 144), (8, 264, 272), (9, 248, 4096),
+                                   (33, 512, 1040), (100, 1000, 336), (128, 256, 512), (129, 392, 640),
+                                   (300, 2056, 2064), (1000, 128, 128), (2, 4096, 7168)])
+def test_product_dense(M, N, K, dtype):
+    check_product(1, M, N, K, None, dtype)
+
+
+@pytest.mark.parametrize("E,M,N,K,offsets", [
+    (4, 300, 264, 272, [0, 0, 129, 129, 300]),           # empty experts first and in the middle
+    (3, 50, 128, 128, [0, 0, 0, 0]),                     # no rows at all
+    (3, 50, 136, 400, [5, 6, 30, 41]),                   # rows before the first and behind the last stay
+    (2, 1, 40, 16, [0, 1, 1]),
+    (5, 700, 520, 256, [0, 1, 9, 265, 640, 700]),
+    (64, 640, 256, 512, list(range(0, 650, 10))),
+    (256, 300, 72, 144, [min(300, 2 * i) for i in range(257)])])
+def test_product_by_expert(E, M, N, K, offsets):
+    check_product(E, M, N, K, offsets)
+    check_product(E, M, N, K, offsets, torch.float32, seed=50)
+
+
+def test_product_offsets_out_of_order_are_clamped():
+    """Offsets beyond M count as M, descending ones as the one before."""
+    a, sa = rows8(40, 128, 1)
+    w, sw = weight8(3, 64, 128, 2)
+    out = torch.zeros(40, 64, dtype=torch.float32, device="cuda")
+    moe.gemm_fp8(a, sa, w, sw, out, offsets=torch.tensor([-5, 20, 10, 900], dtype=torch.int32, device="cuda"))
+    want = torch.zeros_like(out)
+    moe.gemm_fp8(a, sa, w, sw, want, offsets=torch.tensor([0, 20, 20, 40], dtype=torch.int32, device="cuda"))
+    assert torch.equal(out, want) and bool(out.abs().sum() > 0)
+
+
+def test_product_zero_scales_and_nan_rows():
+    """A NaN stays in its row; blocks of scale zero add nothing."""
+    a, sa = rows8(70, 384, 1)
+    w, sw = weight8(1, 136, 384, 2)
+    a[9, 200] = NAN
+    sa[:, 1] = 0.0
+    sa[9, 1] = 1.0
+    out = torch.empty(70, 136, device="cuda")
+    moe.gemm_fp8(a, sa, w, sw, out)
+    assert out[9].isnan().all() and not out[torch.arange(70, device="cuda") != 9].isnan().any()
+
+
+# ------------------------------------------------------------------ experts
+def make_experts(T, D, F, E, K, seed=0):
+    x, xs = rows8(T, D, seed)
+    gu = (randn(E, 2 * F, D, seed=seed + 2) * 100).clamp(-448, 448).to(F8)
+    gus = (torch.rand(E, 2, R.nblk(F), R.nblk(D), generator=gen(seed + 3), device="cuda") + 0.5) / 100 / D ** 0.5
+    dn, dns = weight8(E, D, F, seed + 4, std=F ** -0.5)
+    sel = torch.rand(T, E, generator=gen(seed + 5), device="cuda").topk(K, 1).indices
+    w = torch.rand(T, K, generator=gen(seed + 6), device="cuda")
+    return [x, xs, sel, w, gu, gus, dn, dns]
+
+
+def run_experts(args, stream=None):
+    x, sel, dn = args[0], args[2], args[6]
+    T, D = x.shape
+    E, _, F = dn.shape
+    ws = torch.full((moe.experts_workspace_size_fp8(T, D, F, E, sel.shape[1]),), 255, dtype=torch.uint8,
+                    device="cuda")             # garbage: nothing of it may be relied on
+    out = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+    moe.experts_forward_fp8(*args, out, workspace=ws, stream=stream)
+    return out
+
+
+def check_experts(args, out):
+    want, raw, bound = R.experts(*args)
+    K = args[2].shape[1]
+    # half a step of the intermediate's e4m3, the two roundings to bf16 (each expert's and the sum's)
+    mag = want.abs() + bound
+    each = sum((args[3][:, k:k + 1].double().abs() for k in range(K)))
+    cap = raw.abs().amax(1, keepdim=True) + bound.amax(1, keepdim=True)
+    tol = bound * 1.01 + mag * 2.0 ** -8 * 1.01 + each.clamp_min(1) * cap * 2.0 ** -7 + 1e-6
+    assert ((out.double() - raw).abs() <= tol).all()
+    # against the rounded intermediate: what is left are the bf16 roundings (2^-8 each at most) and the few
+    # values that fall on the other side of a border (a share of 1e-4, each 2^-4 off: 6e-4 in the norm)
+    d = (out.double() - want).norm() / want.norm().clamp_min(1e-30)
+    assert d <= 2.0 ** -8 + 2.0 ** -8 + 1e-3, float(d)
+
+
+@pytest.mark.parametrize("T,D,F,E,K", [(1, 16, 16, 1, 1), (1, 256, 384, 8, 2), (3, 144, 272, 4, 4), (32, 512, 1408, 64, 6),
+                                       (5, 128, 128, 256, 8), (200, 272, 400, 8, 2), (700, 256, 128, 4, 3),
+                                       (2100, 128, 144, 64, 2), (129, 1024, 256, 1, 1)])
+def test_experts(T, D, F, E, K):
+    args = make_experts(T, D, F, E, K)
+    out = run_experts(args)
+    check_experts(args, out)
+    assert torch.equal(out, run_experts(args))
+
+
+@pytest.mark.parametrize("T", [7, 400])
+def test_experts_unused_slots_and_repeats(T):
+    """Slots outside [0, E) add nothing whatever their weight; a repeated expert counts twice; all to one expert."""
+    args = make_experts(T, 256, 272, 8, 3, seed=20)
+    sel, w = args[2], args[3]
+    sel[0] = -1                                  # a padded token
+    w[0] = NAN
+    sel[1, 1], w[1, 1] = 8, INF
+    sel[2] = sel[2, 0]
+    sel[3, 2] = 2 ** 40
+    out = run_experts(args)
+    assert (out[0] == 0).all()
+    args[3] = torch.where((sel < 0) | (sel >= 8), torch.zeros_like(w), w)
+    check_experts(args, out)
+    sel[:] = 5
+    check_experts(args, run_experts(args))
+    sel[:] = -1
+    assert (run_experts(args) == 0).all()
+
+
+def test_experts_streams_graph_and_shared_workspace():
+    """Another stream; two captured calls that share a workspace, replayed with new inputs."""
+    args, other = make_experts(24, 256, 384, 8, 2, seed=1), make_experts(300, 256, 384, 8, 2, seed=2)
+    want, want2 = run_experts(args), run_experts(other)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        assert torch.equal(run_experts(args), want)
+    s.synchronize()
+    ws = torch.empty(max(moe.experts_workspace_size_fp8(T, 256, 384, 8, 2) for T in (24, 300)), dtype=torch.uint8,
+                     device="cuda")
+    out, out2 = torch.empty_like(want), torch.empty_like(want2)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.experts_forward_fp8(*args, out, workspace=ws)
+        moe.experts_forward_fp8(*other, out2, workspace=ws)
+    for _ in range(2):
+        out.zero_(), out2.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(out2, want2)
+    fresh = make_experts(24, 256, 384, 8, 2, seed=7)
+    for a, b in zip(args, fresh):
+        a.copy_(b)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, run_experts(fresh))
+
+
+def test_small_calls_capture():
+    """The norm, the choice and the product in one graph."""
+    x, r, w = randn(9, 256, seed=1).bfloat16(), randn(9, 256, seed=2).bfloat16(), randn(256, seed=3).bfloat16()
+    want = run_norm(x, r, w, 1e-6)
+    wt, sw = weight8(1, 64, 256, 4)
+    lg = randn(9, 64, seed=5)
+    o = run_norm(x, r, w, 1e-6)
+    out, ref = torch.empty(9, 64, device="cuda"), torch.empty(9, 64, device="cuda")
+    sel, ww = torch.empty(9, 4, dtype=torch.int64, device="cuda"), torch.empty(9, 4, device="cuda")
+
+    def step(dst):
+        moe.add_rmsnorm(x, w, 1e-6, residual=r, **o)
+        moe.gemm_fp8(o["out8"], o["scales"], wt, sw, dst)
+        moe.select_experts(lg, 4, True, sel, ww)
+
+    step(ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(out)
+    for v in o.values():
+        v.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[k].view(torch.uint8), want[k].view(torch.uint8)) for k in o)
+    assert torch.equal(out, ref) and torch.equal(sel, R.select(lg, 4, True)[0])
+
+
+def test_profiler_counts_the_call():
+    args = make_experts(16, 256, 256, 4, 2)
+    run_experts(args)
+    moe.profile_enable(True)
+    run_experts(args)
+    run_experts(args)
+    ms, calls = moe.profile_read()
+    moe.profile_enable(False)
+    assert calls == 2
+    assert all(ms[k] > 0 for k in ("permute", "gate_up", "down", "combine")) and ms["router"] == 0
+
+
+# -------------------------------------------------------------------- block
+@pytest.mark.parametrize("T,D,F,E,K,residual", [(1, 256, 384, 16, 4, True), (77, 272, 400, 16, 4, True),
+                                                (600, 256, 256, 8, 2, False)])
+def test_block(T, D, F, E, K, residual):
+    """Norm, routing with groups and experts together, each step against float64 on what the step before gave."""
+    bf = torch.bfloat16
+    router, gu = randn(E, D, seed=1, std=0.1).to(bf), randn(E, 2 * F, D, seed=2, std=D ** -0.5).to(bf)
+    dn = randn(E, D, F, seed=3, std=F ** -0.5).to(bf)
+    nw = (1 + 0.1 * randn(D, seed=4)).to(bf) if residual else None
+    o = dict(score="sigmoid", selection_bias=0.1 * randn(E, seed=5), groups=4, top_groups=2, group_score="top2", scale=2.5)
+    blk = moe.MoEBlockFP8(router, gu, dn, top_k=K, norm_weight=nw, **o)
+    x, r = randn(T, D, seed=6).to(bf), randn(T, D, seed=7).to(bf)
+    out = blk(x, r) if residual else blk(x)
+    y, y64 = x, x.double()
+    if residual:
+        h, y64 = R.add_rmsnorm(x, r, nw, 1e-6)
+        assert torch.equal(blk.residual_, h)
+        y = y64.to(bf)
+    lg = y.double() @ router.double().T
+    assert ((blk.router_logits_.double() - lg).abs() <= (y.double().abs() @ router.double().abs().T) * 2.0 ** -7).all()
+    sel, w = R.select(blk.router_logits_, K, True, **o)
+    assert torch.equal(sel, blk.selected_experts_)
+    # the layer in 64 bits on unrounded weights: 8-bit values are off by 2^-4 at most each (2^-5 to 2^-6 on average,
+    # independent); of x, gate, up, h and down together under 2^-3 in the norm
+    X = y64
+    want = torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    for k in range(K):
+        g, u = (torch.einsum("td,tfd->tf", X, gu.view(E, 2, F, D)[sel[:, k], i].double()) for i in (0, 1))
+        want += w[:, k:k + 1] * torch.einsum("tf,tdf->td", g * torch.sigmoid(g) * u, dn[sel[:, k]].double())
+    assert (out.double() - want).norm() <= 2.0 ** -3 * want.norm()
+    again = blk(x, r) if residual else blk(x)
+    assert torch.equal(out, again)
