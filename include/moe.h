@@ -511,7 +511,7 @@ MOE_API moe_status_t moe_device_status(void* stream);
  * whether and where a bounded wait has given up.  Bit 0 = a wait timed out;
  * bits 8.. = the site (router / grouped GEMM / CTA-pair GEMM, each as
  * producer, MMA issuer or epilogue, then the test probe, then the 8-bit
- * GEMM's three roles).  *word is host
+ * GEMM's four roles).  *word is host
  * memory.  Returns MOE_OK, MOE_ERR_INVALID_ARG (word NULL) or MOE_ERR_CUDA.
  */
 MOE_API moe_status_t moe_device_error_peek(unsigned int* word);

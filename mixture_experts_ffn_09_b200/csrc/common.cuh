@@ -38,6 +38,7 @@ enum : unsigned int {
   SITE_FP8_PRODUCER = 1u << 18,
   SITE_FP8_MMA = 1u << 19,
   SITE_FP8_EPILOGUE = 1u << 20,
+  SITE_FP8_SCALES = 1u << 21,
 };
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
@@ -162,6 +163,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       }
     }
   }
+}
+
+// One try that waits up to about 1 ms inside the instruction (the suspend
+// hint, capped there).  For waits on a short loop's critical path: two warps
+// that signal each other with it take 44 cycles a round trip, with a loop of
+// plain tries 140, with mbar_wait above 230.  False is not final: go on with
+// mbar_wait, out of the usual path.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
 }
 
 // The same wait with cluster-scope acquire: for a barrier that a thread of

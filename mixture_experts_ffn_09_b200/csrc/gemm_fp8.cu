@@ -7,31 +7,47 @@
 // fresh fp32 accumulator in TMEM; the scales differ from block to block in
 // both operands, so the outer sum is kept in fp32 registers: the epilogue
 // warps read each block's accumulator and add it, times sa * sw, to their
-// own.  The tensor cores work on block kb + 1 in the other half of TMEM
-// meanwhile.
+// own, while the tensor cores work on the next ones.
 //
-// One persistent CTA per SM, 320 threads:
-//   warp 0      TMA producer: A tile 128 x 128 and B tile 256 x 128 (two
-//               128-row boxes) per block into a 4-stage ring.  A row block
-//               of few rows is loaded by a lower box (8 to 128 rows); the
-//               rest of the stage keeps what it held and feeds only
-//               accumulator rows that are never read;
-//   warp 1      allocates 512 TMEM columns; one lane issues the MMAs
-//               (M = 128, N = 256) into two 256-column accumulators in turn;
-//   warps 2..9  epilogue: a warp reads its 32 TMEM lanes (rows) and half of
-//               the columns: 64 of the first 128 and 64 of the second, so
-//               that in the gated form it holds the gate and the up value
-//               of the same features.  128 fp32 sums per thread.
+// A tile is 128 rows (256 on a CTA pair) x 256 weight rows.  What limits such
+// a kernel is the round trip accumulator ready -> read -> free -> next MMA,
+// some 1100 cycles long with 256 columns against the 512 that a block's MMAs
+// take, and the epilogue warps' own chain of waits.  So the 256 columns are
+// two halves of 128 that run apart from each other: an MMA warp, two TMEM
+// buffers and four epilogue warps each.
+//
+// One persistent CTA per SM (or pair of CTAs per two SMs), 384 threads:
+//   warp 0      TMA producer: A tile 128 x 128 and B rows (256, or this CTA's
+//               128 of a pair) x 128 per block into a ring.  Without a pair,
+//               a row block of few rows is loaded by a lower box (8 to 128
+//               rows); the rest of the stage keeps what it held and feeds
+//               only accumulator rows that are never read;
+//   warps 1, 2  issue the MMAs of one half each (M = 128 or 256, N = 128);
+//               warp 1 allocates the 512 TMEM columns;
+//   warp 3      scale loader: 8 blocks' scales of the CTA's 128 rows at a
+//               time, read along the rows and left by block in shared memory
+//               (two such groups), so that an epilogue warp's read is one
+//               conflict-free access;
+//   warps 4..11 epilogue: four warps per half, 32 TMEM lanes (rows) each, all
+//               128 columns of the half: 128 fp32 sums per thread.
+// Registers move from warps 0..3 (72 each) to the epilogue (216): 128 * 72 +
+// 256 * 216 of the launch's 384 * 168.
+//
+// A half is 64 rows of the first 128-row weight block and 64 of the second,
+// so in the gated form (B = 128 gate rows and the matching 128 up rows) it
+// holds the gate and the up value of the same 64 features.  On a pair each
+// CTA stages its own A rows and one of the two weight blocks (cta_group::2
+// reads both CTAs' shared memory): 32 KB per block and CTA instead of 48.
 //
 // Epilogues (columns of the output per tile):
 //   kOutBf16, kOutF32   the sums, rounded once (256 columns);
-//   kSiluQuant    B = 128 gate rows and the matching 128 up rows; h =
-//                 silu(gate) * up in fp32, then e4m3 with one scale for the
-//                 row's 128 columns: a row's largest |h| is a maximum over
-//                 two threads (128 columns).
+//   kSiluQuant          h = silu(gate) * up in fp32, then e4m3 with one scale
+//                       for the row's 128 columns: a row's largest |h| is a
+//                       maximum over the two threads (halves) that share it.
 //
 // Rows outside [offsets[0], offsets[E]) are not touched.  Every mbarrier wait
-// is bounded (common.cuh).
+// is bounded (common.cuh); after a timeout the epilogue runs through its loop
+// without waiting, so that no warp is left at a barrier.
 #include <mutex>
 
 #include "common.cuh"
@@ -41,17 +57,28 @@
 namespace moe {
 namespace {
 
-constexpr int BM = 128;
+constexpr int BM = 128;                        // rows per CTA
 constexpr int BK = 128;                        // bytes = e4m3 values = one scale block
-constexpr int BN = 256;
-constexpr int STAGES = 4;
+constexpr int BN = 256;                        // weight rows per tile
+constexpr int BH = 128;                        // columns of a half
 constexpr int A_BYTES = BM * BK;               // 16 KB
-constexpr int B_BYTES = BN * BK;               // 32 KB
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int EPI_WARP0 = 4;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int SCALE_KB = 8;                    // blocks per group of scales
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kBoxes = 5;                      // A boxes of 8, 16, 32, 64 and 128 rows
+constexpr int kRowGroup = 16;                  // row blocks that share a pass over the weights
+
+constexpr long long kPairRows = 192;           // rows per expert from which pairs run
+
+template <bool PAIR>
+struct Cfg {
+  static constexpr int STAGES = PAIR ? 6 : 4;
+  static constexpr int B_BYTES = (PAIR ? BN / 2 : BN) * BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int TILE_M = PAIR ? 2 * BM : BM;
+};
 
 enum { kOutBf16 = 0, kOutF32 = 1, kSiluQuant = 2 };
 
@@ -77,33 +104,135 @@ struct Params {
   unsigned int* err;
 };
 
+template <bool PAIR>
 struct Tail {
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
-  uint64_t tfull[2];
-  uint64_t tempty[2];
+  uint64_t full[Cfg<PAIR>::STAGES];    // the stage is loaded (pair: the leader's, for both CTAs)
+  uint64_t empty[Cfg<PAIR>::STAGES];   // both halves' MMAs have read it
+  uint64_t tfull[2][2];                // [half][buffer] accumulator ready
+  uint64_t tempty[2][2];               // its readers are done (pair: the leader's, for both CTAs)
   uint64_t xfull[2];        // gated: every epilogue warp has written its amax[tile parity]
-  uint64_t mma_done;
+  uint64_t sfull[2];        // a group of scales is in place
+  uint64_t sempty[2];       // every epilogue warp is done with it
+  uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort;
   int total_tiles;
   int tile_start[kMaxExperts + 1];
   int off[kMaxExperts + 1];
-  float amax[2][2][BM];     // [tile parity][column half][row]
+  alignas(16) float amax[2][2][BM];     // [tile parity][half][row]
+  alignas(16) float sa[2][SCALE_KB][BM];
+  alignas(16) float2 sw[2][SCALE_KB];   // of the first and the second 128 weight rows
 };
 
-constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + sizeof(Tail);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+template <bool PAIR>
+constexpr size_t smem_bytes() {
+  return 1024 + Cfg<PAIR>::STAGES * Cfg<PAIR>::STAGE_BYTES + sizeof(Tail<PAIR>);
+}
+static_assert(smem_bytes<false>() <= 227 * 1024 && smem_bytes<true>() <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_to_rank0(const void* p) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+// An arrival where `on` holds, as a predicated instruction instead of a branch.
+__device__ __forceinline__ void arrive_if(bool on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
+// The same on a barrier of the pair's leader.  What it hands over are TMEM
+// columns that tcgen05.wait::ld has seen read, no memory: a release at cluster
+// scope would flush this thread's accesses, 1300 cycles in the epilogue's loop.
+__device__ __forceinline__ void arrive_if_cluster(bool on, uint32_t cluster_addr) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
+      "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs, fp32 accumulator.
+template <bool PAIR>
 __device__ __forceinline__ void umma_fp8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives once on `bar` (of both CTAs of a pair) when the MMAs that this
+// thread has issued are complete.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_get(uint32_t* dst) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, TMEM_COLS);
+    tmem_relinquish();
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t taddr) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(TMEM_COLS)
+                 : "memory");
+  else
+    tmem_dealloc(taddr, TMEM_COLS);
+}
+
+// Tiled load whose bytes are counted on the barrier at `bar` (a cluster
+// address; of a pair the leader's).
+template <bool PAIR>
+__device__ __forceinline__ void load_box(const CUtensorMap* map, uint32_t bar, void* dst, int c0, int c1) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
 }
 
 // Instruction descriptor of kind::f8f6f4: e4m3 A and B (format 0), both
@@ -112,26 +241,19 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// Waits for the loads issued so far; v is what the last one filled, so that
-// no use of it moves ahead of the wait.
-__device__ __forceinline__ void tmem_wait16(uint32_t (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
-                 "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
-                 "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
-               : "memory");
+// Waits for the TMEM loads issued so far; a and b are what they filled, so
+// that no use of them moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait(uint32_t (&a)[32], uint32_t (&b)[32]) {
+#define V8(v, i) \
+  "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), \
+      "+r"(v[i + 6]), "+r"(v[i + 7])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {    // (an asm statement takes 30 operands, "+r" counting twice)
+    asm volatile("" : V8(a, i));
+    asm volatile("" : V8(b, i));
+  }
+#undef V8
 }
 
 // Four rows of A (128 columns from c0) into 512 contiguous bytes with the
@@ -146,37 +268,51 @@ __device__ __forceinline__ void tma_gather4(const CUtensorMap* map, uint64_t* ba
       : "memory");
 }
 
-// acc + v * s on two neighbouring columns at once.
-__device__ __forceinline__ void fma2(float2& acc, uint32_t v0, uint32_t v1, float s) {
-  asm("{\n\t.reg .b64 a, b, c;\n\t"
-      "mov.b64 a, {%2, %3};\n\t"
-      "mov.b64 b, {%4, %4};\n\t"
-      "mov.b64 c, {%0, %1};\n\t"
-      "fma.rn.f32x2 c, a, b, c;\n\t"
-      "mov.b64 {%0, %1}, c;\n\t}"
-      : "+f"(acc.x), "+f"(acc.y)
-      : "r"(v0), "r"(v1), "f"(s));
+// Two neighbouring columns in one 64-bit register.  fma.rn.f32x2 does the work
+// of two FMAs in one issue slot (at their rate, two cycles): the epilogue's
+// issue slots are scarce.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 both(float s) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
+  return r;
+}
+__device__ __forceinline__ void fma2(f32x2& acc, uint32_t x, uint32_t y, f32x2 s) {
+  f32x2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(x), "r"(y));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+}
+__device__ __forceinline__ float2 unpack(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
 }
 
 struct Tile {
-  int e, row0, rows, n_blk;    // rows of the expert left from row0 on (may exceed BM)
+  int e, row0, rows, n_blk;    // rows of the expert left from row0 on (may exceed the tile's)
 };
 
-// Tiles of an expert: row block fastest, so CTAs side by side share a
-// weight tile through L2.
-__device__ __forceinline__ Tile decode_tile(const Tail* st, int E, int n_tiles, int t) {
+// Tiles of an expert: in groups of kRowGroup row blocks, weight block by
+// weight block, the row block fastest.  CTAs side by side then share weight
+// tiles through L2, and a group's rows stay there while the weights pass by
+// once per group.
+__device__ __forceinline__ Tile decode_tile(const int* tile_start, const int* off, int E, int n_tiles,
+                                            int tile_m, int t) {
   int lo = 0, hi = E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (st->tile_start[mid] <= t) lo = mid; else hi = mid - 1;
+    if (tile_start[mid] <= t) lo = mid; else hi = mid - 1;
   }
   Tile r;
   r.e = lo;
-  const int local = t - st->tile_start[lo];
-  const int mt = (st->tile_start[lo + 1] - st->tile_start[lo]) / n_tiles;
-  r.n_blk = local / mt;
-  r.row0 = st->off[lo] + (local - r.n_blk * mt) * BM;
-  r.rows = st->off[lo + 1] - r.row0;
+  const int local = t - tile_start[lo];
+  const int mt = (tile_start[lo + 1] - tile_start[lo]) / n_tiles;
+  const int g0 = local / (kRowGroup * n_tiles) * kRowGroup;      // the group's first row block
+  const int in = local - g0 * n_tiles;
+  const int gm = min(kRowGroup, mt - g0);
+  r.n_blk = in / gm;
+  r.row0 = off[lo] + (g0 + in - r.n_blk * gm) * tile_m;
+  r.rows = off[lo + 1] - r.row0;
   return r;
 }
 
@@ -187,34 +323,63 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsig
   mbar_wait(bar, parity, &dummy, err, site);
 }
 
-template <int EPI>
+// Bounded wait, suspended in the instruction where it can be.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* err,
+                                     unsigned int site) {
+  if (__builtin_expect(mbar_try_wait_long(bar, parity), 1)) return true;
+  return mbar_wait(bar, parity, abort, err, site);
+}
+
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+template <int EPI, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ CUtensorMap tmB,
                     const Params p) {
+  using C = Cfg<PAIR>;
+  constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // 1024-byte aligned by its address in the shared window: the same offset in
+  // both CTAs of a pair
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * A_BYTES;
-  Tail* st = reinterpret_cast<Tail*>(smem + STAGES * STAGE_BYTES);
+  Tail<PAIR>* st = reinterpret_cast<Tail<PAIR>*>(smem + STAGES * C::STAGE_BYTES);
 
   constexpr int BN_OUT = EPI == kSiluQuant ? 128 : 256;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x;         // takes tiles worker, worker + workers, ...
+  const int workers = PAIR ? gridDim.x >> 1 : gridDim.x;
   const int E = p.E;
   const int n_tiles = (p.n_out + BN_OUT - 1) / BN_OUT;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&st->full[s], 1);
-      mbar_init(&st->empty[s], 1);
+      mbar_init(&st->empty[s], 2);
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(&st->tfull[a], 1);
-      mbar_init(&st->tempty[a], EPI_WARPS);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&st->tfull[a][b], 1);
+        mbar_init(&st->tempty[a][b], PAIR ? EPI_WARPS : EPI_WARPS / 2);
+      }
       mbar_init(&st->xfull[a], EPI_WARPS);
+      mbar_init(&st->sfull[a], 1);
+      mbar_init(&st->sempty[a], EPI_WARPS);
+      mbar_init(&st->mma_done[a], 1);
     }
-    mbar_init(&st->mma_done, 1);
     st->abort = 0;
+    mbar_fence_init();
     // offsets are device data: kept within [0, M] and in order, so that no
     // address below depends on their being right
     int acc = 0, at = p.offsets ? min(max(p.offsets[0], 0), p.M) : 0;
@@ -222,186 +387,320 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int next = p.offsets ? min(max(p.offsets[e + 1], at), p.M) : p.M;
       st->off[e] = at;
       st->tile_start[e] = acc;
-      acc += (next - at + BM - 1) / BM * n_tiles;
+      acc += (next - at + C::TILE_M - 1) / C::TILE_M * n_tiles;
       at = next;
     }
     st->off[E] = at;
     st->tile_start[E] = acc;
     st->total_tiles = acc;
-    mbar_fence_init();
   }
   if (warp == 0 && lane == 0) tma_prefetch_desc(&tmB);
-  if (warp == 1) {
-    tmem_alloc(&st->tmem_base, TMEM_COLS);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_get<PAIR>(&st->tmem_base);
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();      // the leader's barriers exist before the peer uses them
   tc_fence_after();
 
   const uint32_t tmem = st->tmem_base;
   const int total = st->total_tiles;
   volatile int* abort = &st->abort;
+  auto tile_of = [&](int t) { return decode_tile(st->tile_start, st->off, E, n_tiles, C::TILE_M, t); };
 
+  // (each register split dominates its warps' code, so that the compiler
+  // allots their registers by it)
+  if (warp < EPI_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    // One elected lane, as in the MMA warps; gathered rows are fetched by all.
     int stage = 0;
     uint32_t phase = 0, used = 0, last_parity = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      if (!__shfl_sync(0xffffffffu, lane == 0 ? static_cast<int>(!*abort) : 0, 0)) break;
-      const Tile tl = decode_tile(st, E, n_tiles, t);
-      const int rowB0 = tl.e * p.w_rows + tl.n_blk * BN_OUT;
-      const int rowB1 = EPI == kSiluQuant ? rowB0 + p.up_row : rowB0 + 128;
-      const int rows = min(BM, tl.rows);
-      int tok[4] = {0, 0, 0, 0};
-      int gather_lanes = 0, box = 0, a_bytes;
-      if (p.gather) {
-        gather_lanes = (rows + 3) >> 2;
-        a_bytes = gather_lanes * 512;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = min(4 * lane + i, rows - 1);       // past the last row: that row again
-          tok[i] = __ldg(p.perm + tl.row0 + r) / p.slots;
-        }
+    auto step = [&] {
+      used |= 1u << stage;
+      last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+    };
+    // The stage's weight rows.  Alone, a CTA holds rows 0..63 of both weight
+    // blocks, then rows 64..127 (the halves; the map's box has 64 rows); of a
+    // pair, each CTA holds one block.
+    auto load_b = [&](const Tile& tl, int kb, uint32_t bar) {
+      const int row_b0 = tl.e * p.w_rows + tl.n_blk * BN_OUT;
+      const int row_b1 = EPI == kSiluQuant ? row_b0 + p.up_row : row_b0 + 128;
+      uint8_t* b = sB + stage * C::B_BYTES;
+      if constexpr (PAIR) {
+        load_box<PAIR>(&tmB, bar, b, kb * BK, rank == 0 ? row_b0 : row_b1);
       } else {
-        while ((8 << box) < rows) ++box;
-        a_bytes = (8 << box) * BK;
+        load_box<PAIR>(&tmB, bar, b, kb * BK, row_b0);
+        load_box<PAIR>(&tmB, bar, b + 64 * BK, kb * BK, row_b1);
+        load_box<PAIR>(&tmB, bar, b + 128 * BK, kb * BK, row_b0 + 64);
+        load_box<PAIR>(&tmB, bar, b + 192 * BK, kb * BK, row_b1 + 64);
       }
-      bool ok = true;
-      for (int kb = 0; kb < p.num_kb; ++kb) {
-        int good = 1;
-        if (lane == 0) {
-          good = mbar_wait(&st->empty[stage], phase ^ 1u, abort, p.err, SITE_FP8_PRODUCER) ? 1 : 0;
-          if (good) mbar_arrive_expect_tx(&st->full[stage], a_bytes + B_BYTES);
-        }
-        if (!__shfl_sync(0xffffffffu, good, 0)) { ok = false; break; }
-        if (lane < gather_lanes)
-          tma_gather4(&tmA.m[0], &st->full[stage], sA + stage * A_BYTES + lane * 512, kb * BK, tok[0],
-                      tok[1], tok[2], tok[3]);
-        if (lane == 0) {
-          if (!p.gather)
-            tma_load_2d(&tmA.m[box], &st->full[stage], sA + stage * A_BYTES, kb * BK, tl.row0);
-          tma_load_2d(&tmB, &st->full[stage], sB + stage * B_BYTES, kb * BK, rowB0);
-          tma_load_2d(&tmB, &st->full[stage], sB + stage * B_BYTES + B_BYTES / 2, kb * BK, rowB1);
-          used |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-        }
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-      }
-      if (!ok) break;
-    }
-    // let every issued load land before the CTA can leave
-    if (lane == 0)
-      for (int s = 0; s < STAGES; ++s)
-        if (used & (1u << s)) drain_wait(&st->full[s], (last_parity >> s) & 1u, p.err, SITE_FP8_PRODUCER);
-  } else if (warp == 1) {
-    // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(BM, BN);
-      int stage = 0;
-      uint32_t phase = 0, i = 0;                  // i: blocks issued so far
-      bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        for (int kb = 0; kb < p.num_kb; ++kb, ++i) {
-          const uint32_t acc = i & 1u;
-          if (!mbar_wait(&st->tempty[acc], ((i >> 1) & 1u) ^ 1u, abort, p.err, SITE_FP8_MMA) ||
-              !mbar_wait(&st->full[stage], phase, abort, p.err, SITE_FP8_MMA)) {
+    };
+    bool ok = true;
+    if (!PAIR && p.gather) {
+      for (int t = worker; t < total && ok; t += workers) {
+        const Tile tl = tile_of(t);
+        const int rows = min(BM, tl.rows);
+        const int fetchers = (rows + 3) >> 2;    // lanes with rows, four each
+        int tok[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)              // past the last row: that row again
+          tok[i] = __ldg(p.perm + tl.row0 + min(4 * lane + i, rows - 1)) / p.slots;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!__all_sync(0xffffffffu, wait(&st->empty[stage], phase ^ 1u, abort, p.err, SITE_FP8_PRODUCER))) {
             ok = false;
             break;
           }
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&st->full[stage], fetchers * 512 + C::B_BYTES);
+            load_b(tl, kb, smem_u32(&st->full[stage]));
+          }
+          __syncwarp();        // the bytes are expected before any row can land
+          if (lane < fetchers)
+            tma_gather4(&tmA.m[0], &st->full[stage], sA + stage * A_BYTES + lane * 512, kb * BK, tok[0],
+                        tok[1], tok[2], tok[3]);
+          step();
+        }
+      }
+      used = lane == 0 ? used : 0u;
+    } else if (elect_one()) {
+      for (int t = worker; t < total && ok; t += workers) {
+        const Tile tl = tile_of(t);
+        int box = kBoxes - 1;
+        if constexpr (!PAIR)
+          for (box = 0; (8 << box) < min(BM, tl.rows);) ++box;
+        const uint32_t tx = PAIR ? 2 * C::STAGE_BYTES : (8 << box) * BK + C::B_BYTES;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (__builtin_expect(!wait(&st->empty[stage], phase ^ 1u, abort, p.err, SITE_FP8_PRODUCER), 0)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&st->full[stage], tx);
+          const uint32_t bar = PAIR ? map_to_rank0(&st->full[stage]) : smem_u32(&st->full[stage]);
+          load_box<PAIR>(&tmA.m[box], bar, sA + stage * A_BYTES, kb * BK,
+                         tl.row0 + static_cast<int>(rank) * BM);
+          load_b(tl, kb, bar);
+          step();
+        }
+      }
+    }
+    // Let every issued load land before the CTA can leave: the leader sees
+    // them on its full barriers; a peer's complete on the leader's, so the
+    // peer waits for the MMAs to have released its stages.
+    for (int s = 0; s < STAGES; ++s)
+      if (used & (1u << s))
+        drain_wait(rank == 0 ? &st->full[s] : &st->empty[s], (last_parity >> s) & 1u, p.err,
+                   SITE_FP8_PRODUCER);
+  } else if (warp < 3) {
+    // ----------------------------------------------------------------- MMA
+    // One elected lane runs the loop: elect.sync tells the compiler that the
+    // operands of tcgen05.mma are uniform (with `lane == 0` an issue takes
+    // three times as long).
+    const int half = warp - 1;
+    constexpr uint32_t idesc = idesc_e4m3_f32(C::TILE_M, BH);
+    if (rank == 0 && elect_one()) {
+      const uint64_t da = sw128_kmajor_desc(smem_u32(sA));
+      const uint64_t db = sw128_kmajor_desc(smem_u32(sB) + half * (PAIR ? 64 : 128) * BK);
+      const uint32_t d0 = tmem + half * 2 * BH;
+      int stage = 0;
+      uint32_t phase = 0, i = 0;                  // i: blocks issued so far
+      bool ok = true;
+      for (int t = worker; t < total && ok; t += workers) {
+        for (int kb = 0; kb < p.num_kb; ++kb, ++i) {
+          const uint32_t buf = i & 1u;
+          const uint32_t tpar = ((i >> 1) & 1u) ^ 1u;
+          const bool loaded = mbar_try_wait_long(&st->full[stage], phase);
+          const bool free = mbar_try_wait_long(&st->tempty[half][buf], tpar);
+          if (__builtin_expect(!(loaded && free), 0)) {
+            if (!mbar_wait(&st->full[stage], phase, abort, p.err, SITE_FP8_MMA) ||
+                !mbar_wait(&st->tempty[half][buf], tpar, abort, p.err, SITE_FP8_MMA)) {
+              ok = false;
+              break;
+            }
+          }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + stage * A_BYTES);
-          const uint32_t b0 = smem_u32(sB + stage * B_BYTES);
 #pragma unroll
-          for (int k = 0; k < BK / 32; ++k)
-            umma_fp8(tmem + acc * BN, sw128_kmajor_desc(a0 + k * 32), sw128_kmajor_desc(b0 + k * 32),
-                     idesc, k != 0 ? 1u : 0u);
-          umma_commit(&st->empty[stage]);
-          umma_commit(&st->tfull[acc]);
+          for (int k = 0; k < BK / 32; ++k)      // 32 bytes further: +2 in 16-byte units
+            umma_fp8<PAIR>(d0 + buf * BH, da + (stage * A_BYTES >> 4) + 2 * k,
+                           db + (stage * C::B_BYTES >> 4) + 2 * k, idesc, k != 0 ? 1u : 0u);
+          commit<PAIR>(&st->tfull[half][buf]);
+          commit<PAIR>(&st->empty[stage]);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
       // all MMAs issued by this thread complete before TMEM / smem go away
-      umma_commit(&st->mma_done);
-      drain_wait(&st->mma_done, 0, p.err, SITE_FP8_MMA);
+      commit<PAIR>(&st->mma_done[half]);
+      drain_wait(&st->mma_done[half], 0, p.err, SITE_FP8_MMA);
     }
-  } else {
-    // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3;                   // TMEM lanes this warp may access
-    const int half = (warp - 2) >> 2;
-    const int r = quad * 32 + lane;              // row of the tile
-    const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
-    uint32_t i = 0;                              // blocks read so far
-    bool ok = true;
-    int n = 0;                                   // tiles begun before this one
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++n) {
-      const int parity = n & 1;
-      const Tile tl = decode_tile(st, E, n_tiles, t);
-      const bool live = quad * 32 < tl.rows;     // warp-uniform
-      const bool rvalid = r < tl.rows;
-      const int grow = tl.row0 + (rvalid ? r : 0);
-      const int srow = p.perm ? __ldg(p.perm + grow) / p.slots : grow;
-      const float* sa = p.sa + static_cast<size_t>(srow) * p.num_kb;
+  } else if (warp == 3) {
+    // -------------------------------------------------------- scale loader
+    // A group's loads are issued before the wait for its place in shared
+    // memory, so that their latency passes while the group before is used.
+    const bool vec = (p.num_kb & 3) == 0;        // a row's scales start at 16 bytes
+    const int k = lane & 7;                      // lanes 0..7: the first weight block's, 8..15: the second's
+    const float* sw = nullptr;
+    const float* sa[4];
+    float va[4][SCALE_KB], vw = 0.f;
+    auto point = [&](int t) {                    // at tile t
+      const Tile tl = tile_of(t);
       const int b0 = EPI == kSiluQuant ? tl.n_blk : 2 * tl.n_blk;
       const int b1 = EPI == kSiluQuant ? p.up_block + tl.n_blk : min(b0 + 1, p.w_blocks - 1);
-      const float* sw0 = p.sw + (static_cast<size_t>(tl.e) * p.w_blocks + b0) * p.num_kb;
-      const float* sw1 = p.sw + (static_cast<size_t>(tl.e) * p.w_blocks + b1) * p.num_kb;
-      float2 acc[64];                            // [0, 32) the first 64 columns, [32, 64) the second
+      sw = p.sw + (static_cast<size_t>(tl.e) * p.w_blocks + (lane & 8 ? b1 : b0)) * p.num_kb;
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      float na = __ldg(sa), n0 = __ldg(sw0), n1 = __ldg(sw1);
-      for (int kb = 0; kb < p.num_kb; ++kb, ++i) {
-        const float s0 = na * n0, s1 = na * n1;
-        if (kb + 1 < p.num_kb) {                 // the next block's scales, behind this one's wait
-          na = __ldg(sa + kb + 1);
-          n0 = __ldg(sw0 + kb + 1);
-          n1 = __ldg(sw1 + kb + 1);
-        }
-        const uint32_t buf = i & 1u;
-        // every lane must agree before the warp-collective TMEM loads
-        const bool got = mbar_wait(&st->tfull[buf], (i >> 1) & 1u, abort, p.err, SITE_FP8_EPILOGUE);
-        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+      for (int h = 0; h < 4; ++h) {              // past the last row: that row again
+        const int grow = tl.row0 + min(static_cast<int>(rank) * BM + h * 32 + lane, tl.rows - 1);
+        sa[h] = p.sa + static_cast<size_t>(p.perm ? __ldg(p.perm + grow) / p.slots : grow) * p.num_kb;
+      }
+    };
+    auto fetch = [&](int k0) {                   // past the last block: that block again
+      if (vec) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int q = 0; q < SCALE_KB / 4; ++q) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(sa[h] + min(k0 + 4 * q, p.num_kb - 4)));
+            va[h][4 * q] = v.x;
+            va[h][4 * q + 1] = v.y;
+            va[h][4 * q + 2] = v.z;
+            va[h][4 * q + 3] = v.w;
+          }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int q = 0; q < SCALE_KB; ++q) va[h][q] = __ldg(sa[h] + min(k0 + q, p.num_kb - 1));
+      }
+      vw = __ldg(sw + min(k0 + k, p.num_kb - 1));
+    };
+    int t = worker, k0 = 0;
+    if (t < total) {
+      point(t);
+      fetch(0);
+    }
+    for (uint32_t g = 0; t < total; ++g) {       // g: groups stored so far
+      const uint32_t buf = g & 1u;
+      if (!__all_sync(0xffffffffu, wait(&st->sempty[buf], ((g >> 1) & 1u) ^ 1u, abort, p.err,
+                                        SITE_FP8_SCALES)))
+        break;
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int q = 0; q < SCALE_KB; ++q) st->sa[buf][q][h * 32 + lane] = va[h][q];
+      if (lane < 16) (lane & 8 ? st->sw[buf][k].y : st->sw[buf][k].x) = vw;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&st->sfull[buf]);
+      k0 += SCALE_KB;
+      if (k0 >= p.num_kb) {
+        k0 = 0;
+        t += workers;
+        if (t < total) point(t);
+      }
+      if (t < total) fetch(k0);
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;                   // TMEM lanes this warp may access
+    const int half = (warp - EPI_WARP0) >> 2;
+    const int r = quad * 32 + lane;              // row of this CTA's 128
+    const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 2 * BH;
+    const uint32_t freed[2] = {PAIR ? map_to_rank0(&st->tempty[half][0]) : 0u,
+                               PAIR ? map_to_rank0(&st->tempty[half][1]) : 0u};
+    uint32_t i = 0;                              // blocks read so far
+    uint32_t g = 0;                              // groups of scales taken so far
+    int n = 0;                                   // tiles begun before this one
+    for (int t = worker; t < total; t += workers, ++n) {
+      const Tile tl = tile_of(t);
+      const int rows = tl.rows - static_cast<int>(rank) * BM;
+      const bool live = quad * 32 < rows;        // warp-uniform
+      const bool rvalid = r < rows;
+      const int grow = tl.row0 + static_cast<int>(rank) * BM + (rvalid ? r : 0);
+      f32x2 acc[2][32];                          // 64 columns of each weight block, in pairs
+#pragma unroll
+      for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0ull;
+      // One block's accumulator, times a * w, onto the sums.  Branches cost
+      // this loop as much as its arithmetic: the wait's usual path has none,
+      // and one lane's arrivals are predicated instructions.
+      auto add_block = [&](uint32_t buf, uint32_t par, float a, float2 w) {
+        const uint32_t src = tb + buf * BH;
+        const bool ready = mbar_try_wait_long(&st->tfull[half][buf], par);
+        __syncwarp();
         tc_fence_after();
+        uint32_t v0[32], v1[32];
+        // The first loads go out before the result of the wait is looked at;
+        // after a wait that had to be taken up again, they are repeated.
         if (live) {
-          const uint32_t src = tb + buf * BN;
-          uint32_t v[2][16];
-          tmem_ld16(src, v[0]);
-          tmem_wait16(v[0]);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {          // 4 chunks of 16 columns of each half
-            if (c < 7) tmem_ld16(src + ((c + 1) >> 2) * 128 + ((c + 1) & 3) * 16, v[(c + 1) & 1]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              fma2(acc[c * 8 + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], c < 4 ? s0 : s1);
-            if (c < 7) tmem_wait16(v[(c + 1) & 1]);
+          tmem_ld32(src, v0);
+          tmem_ld32(src + 32, v1);
+        }
+        const f32x2 s0 = both(a * w.x), s1 = both(a * w.y);
+        if (__builtin_expect(__any_sync(0xffffffffu, !ready), 0)) {
+          mbar_wait(&st->tfull[half][buf], par, abort, p.err, SITE_FP8_EPILOGUE);
+          __syncwarp();
+          tc_fence_after();
+          if (live) {
+            tmem_ld_wait();
+            tmem_ld32(src, v0);
+            tmem_ld32(src + 32, v1);
           }
         }
+        if (live) {
+          tmem_wait(v0, v1);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(acc[0][j], v0[2 * j], v0[2 * j + 1], s0);
+          tmem_ld32(src + 64, v0);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(acc[0][16 + j], v1[2 * j], v1[2 * j + 1], s0);
+          tmem_ld32(src + 96, v1);
+          tmem_wait(v0, v1);
+        }
+        // all of it is in registers: the buffer is free
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&st->tempty[buf]);
+        if constexpr (PAIR) arrive_if_cluster(lane == 0, freed[buf]);
+        else arrive_if(lane == 0, &st->tempty[half][buf]);
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(acc[1][j], v0[2 * j], v0[2 * j + 1], s1);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(acc[1][16 + j], v1[2 * j], v1[2 * j + 1], s1);
+        }
+      };
+      for (int k0 = 0; k0 < p.num_kb; k0 += SCALE_KB, ++g) {
+        const uint32_t sbuf = g & 1u;
+        wait(&st->sfull[sbuf], (g >> 1) & 1u, abort, p.err, SITE_FP8_EPILOGUE);
+        __syncwarp();
+        const float* sa = &st->sa[sbuf][0][r];
+        const float2* sw = st->sw[sbuf];
+        const int nk = min(SCALE_KB, p.num_kb - k0);
+#pragma unroll 1
+        for (int k = 0; k < nk; ++k, ++i) add_block(i & 1u, (i >> 1) & 1u, sa[k * BM], sw[k]);
+        __syncwarp();
+        arrive_if(lane == 0, &st->sempty[sbuf]);
       }
-      if (!ok) break;
 
       if constexpr (EPI == kSiluQuant) {
         // columns [half * 64, half * 64 + 64) of the tile's 128
+        const int parity = n & 1;
         const int col0 = tl.n_blk * 128 + half * 64;
         float m = 0.f;
+        float h[64];
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {
-          const float g = j & 1 ? acc[j >> 1].y : acc[j >> 1].x;
-          const float u = j & 1 ? acc[32 + (j >> 1)].y : acc[32 + (j >> 1)].x;
-          const float v = col0 + j < p.n_out ? silu_bf16_epilogue(g) * u : 0.f;
-          if (j & 1) acc[j >> 1].y = v; else acc[j >> 1].x = v;
-          m = fmaxf(m, fabsf(v));
+        for (int j = 0; j < 32; ++j) {
+          const float2 gt = unpack(acc[0][j]), up = unpack(acc[1][j]);
+          const bool in = col0 + 2 * j < p.n_out;
+          h[2 * j] = in ? silu_bf16_epilogue(gt.x) * up.x : 0.f;
+          h[2 * j + 1] = in ? silu_bf16_epilogue(gt.y) * up.y : 0.f;
+          m = fmaxf(m, fmaxf(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
         }
         st->amax[parity][half][r] = m;
-        // meet the other half's warps (a bounded wait: one of them may have given up)
+        // meet the other half's warps
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->xfull[parity]);
-        if (!__all_sync(0xffffffffu, mbar_wait(&st->xfull[parity], (n >> 1) & 1u, abort, p.err,
-                                               SITE_FP8_EPILOGUE)))
-          break;
-        const float s = fp8_scale(fmaxf(st->amax[parity][0][r], st->amax[parity][1][r]));
+        wait(&st->xfull[parity], (n >> 1) & 1u, abort, p.err, SITE_FP8_EPILOGUE);
+        m = fmaxf(st->amax[parity][0][r], st->amax[parity][1][r]);
+        const float s = fp8_scale(m);
         const float inv = 1.f / s;
         if (rvalid) {
           uint8_t* q = static_cast<uint8_t*>(p.out) + static_cast<size_t>(grow) * p.n_out + col0;
@@ -410,14 +709,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (col0 + 16 * c < p.n_out) {       // n_out is a multiple of 16
               uint32_t w[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = fp8_pack4(acc[8 * c + 2 * j].x * inv, acc[8 * c + 2 * j].y * inv,
-                                 acc[8 * c + 2 * j + 1].x * inv, acc[8 * c + 2 * j + 1].y * inv);
+              for (int j = 0; j < 4; ++j) {
+                const float* f = h + 16 * c + 4 * j;
+                w[j] = fp8_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+              }
               *reinterpret_cast<uint4*>(q + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           if (half == 0)
             p.out_scales[static_cast<size_t>(grow) * ((p.n_out + 127) / 128) + tl.n_blk] = s;
         }
+        __syncwarp();
       } else if (rvalid) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -426,30 +727,38 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 8; ++j) {          // 8 columns: n_out is a multiple of 8
             const int col = col0 + 8 * j;
             if (col >= p.n_out) continue;
-            const float2* a = acc + c * 32 + 4 * j;
+            float a[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float2 f = unpack(acc[c][4 * j + q]);
+              a[2 * q] = f.x;
+              a[2 * q + 1] = f.y;
+            }
             const size_t o = static_cast<size_t>(grow) * p.n_out + col;
             if constexpr (EPI == kOutBf16) {
               uint4 w;
               __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&w);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) b[q] = __floats2bfloat162_rn(a[q].x, a[q].y);
+              for (int q = 0; q < 4; ++q) b[q] = __floats2bfloat162_rn(a[2 * q], a[2 * q + 1]);
               *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) = w;
             } else {
               float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
-              d[0] = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
-              d[1] = make_float4(a[2].x, a[2].y, a[3].x, a[3].y);
+              d[0] = make_float4(a[0], a[1], a[2], a[3]);
+              d[1] = make_float4(a[4], a[5], a[6], a[7]);
             }
           }
         }
       }
+      __syncwarp();
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();      // neither CTA frees TMEM while its peer may still use it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_free<PAIR>(tmem);
   }
 }
 
@@ -487,25 +796,67 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI>
-cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, const Params& p, int grid,
-                       cudaStream_t s) {
-  // the shared-memory opt-in is a per-device function attribute
+// Workers (CTAs or pairs) that the device runs at once; sets the kernel's
+// shared-memory opt-in on the way.  Asked once per device and kernel.
+template <int EPI, bool PAIR>
+cudaError_t resident_workers(int* out) {
   static std::mutex mu;
-  static bool done[64] = {};
+  static int known[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-      err = cudaFuncSetAttribute(gemm_fp8_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kSmemBytes));
-      if (err != cudaSuccess) return err;
-      if (dev >= 0 && dev < 64) done[dev] = true;
-    }
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && dev < 64 && known[dev] > 0) {
+    *out = known[dev];
+    return cudaSuccess;
   }
-  return launch_k(gemm_fp8_kernel<EPI>, dim3(grid), dim3(THREADS), kSmemBytes, s, false, 1, a, b, p);
+  constexpr int bytes = static_cast<int>(smem_bytes<PAIR>());
+  err = cudaFuncSetAttribute(gemm_fp8_kernel<EPI, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err != cudaSuccess) return err;
+  int n = PAIR ? num_sms() / 2 : num_sms();
+  if constexpr (PAIR) {
+    // fewer pairs may fit than half the SMs (a pair shares a GPC)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms() / 2 * 2);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = bytes;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, gemm_fp8_kernel<EPI, PAIR>, &cfg) == cudaSuccess && fit > 0)
+      n = fit < n ? fit : n;
+    else
+      cudaGetLastError();              // the query is advisory
+  }
+  if (dev >= 0 && dev < 64) known[dev] = n;
+  *out = n;
+  return cudaSuccess;
+}
+
+template <int EPI, bool PAIR>
+cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, const Params& p, cudaStream_t s) {
+  int workers = 0;
+  const cudaError_t err = resident_workers<EPI, PAIR>(&workers);
+  if (err != cudaSuccess) return err;
+  const int bn_out = EPI == kSiluQuant ? 128 : 256;
+  const long long n_tiles = (p.n_out + bn_out - 1) / bn_out;
+  // A bound on the tiles; with at most one row block per expert on average
+  // (weight streaming) those of one block per expert.  The grid is then sized
+  // so that every worker takes the same number of tiles.
+  constexpr int tile_m = Cfg<PAIR>::TILE_M;
+  const long long touched = p.M < p.E ? p.M : p.E;
+  long long tiles = (static_cast<long long>(p.M) / tile_m + touched) * n_tiles;
+  if (p.M <= static_cast<long long>(tile_m) * p.E) tiles = touched * n_tiles;
+  const long long waves = (tiles + workers - 1) / workers;
+  int grid = static_cast<int>((tiles + waves - 1) / waves);
+  if (PAIR) grid = 2 * static_cast<int>(tiles < workers ? tiles : workers);
+  return launch_k(gemm_fp8_kernel<EPI, PAIR>, dim3(grid), dim3(THREADS), smem_bytes<PAIR>(), s, false,
+                  PAIR ? 2 : 1, a, b, p);
 }
 
 }  // namespace
@@ -531,28 +882,24 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   p.out = g.out;
   p.out_scales = g.q_scales;
   p.err = g.err;
+  const bool pair = !g.gather && g.M >= kPairRows * g.E;
   AMaps ma;
   CUtensorMap mb;
   for (int i = 0; i < kBoxes; ++i)
     if (!make_map(&ma.m[i], g.a, static_cast<uint64_t>(g.a_rows), static_cast<uint64_t>(g.K),
                   g.gather ? 1u : 8u << i))
       return cudaErrorInvalidValue;
-  if (!make_map(&mb, g.w, static_cast<uint64_t>(g.E) * p.w_rows, static_cast<uint64_t>(g.K), 128u))
+  if (!make_map(&mb, g.w, static_cast<uint64_t>(g.E) * p.w_rows, static_cast<uint64_t>(g.K),
+                pair ? 128u : 64u))
     return cudaErrorInvalidValue;
-  const int bn_out = gated ? 128 : 256;
-  const long long n_tiles = (g.N + bn_out - 1) / bn_out;
-  // With at most 128 rows per expert on average (weight streaming) each
-  // touched expert has one row block: size the grid so that every CTA takes
-  // the same number of tiles.  Else bound the tiles from above.
-  const long long touched = g.M < g.E ? g.M : g.E;
-  long long tiles = (static_cast<long long>(g.M) / BM + touched) * n_tiles;
-  if (g.M <= 128LL * g.E) tiles = touched * n_tiles;
-  const long long sms = num_sms();
-  const long long waves = (tiles + sms - 1) / sms;
-  const int grid = static_cast<int>((tiles + waves - 1) / waves);
-  if (gated) return launch_epi<kSiluQuant>(ma, mb, p, grid, s);
-  if (g.out_f32) return launch_epi<kOutF32>(ma, mb, p, grid, s);
-  return launch_epi<kOutBf16>(ma, mb, p, grid, s);
+  if (pair) {
+    if (gated) return launch_epi<kSiluQuant, true>(ma, mb, p, s);
+    if (g.out_f32) return launch_epi<kOutF32, true>(ma, mb, p, s);
+    return launch_epi<kOutBf16, true>(ma, mb, p, s);
+  }
+  if (gated) return launch_epi<kSiluQuant, false>(ma, mb, p, s);
+  if (g.out_f32) return launch_epi<kOutF32, false>(ma, mb, p, s);
+  return launch_epi<kOutBf16, false>(ma, mb, p, s);
 }
 
 }  // namespace moe

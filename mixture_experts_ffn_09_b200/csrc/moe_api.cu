@@ -666,7 +666,8 @@ const char* moe_error_sites(unsigned int word) {
                                        "gemm producer", "gemm mma", "gemm epilogue",
                                        "pair gemm producer", "pair gemm mma",
                                        "pair gemm epilogue", "bounded-wait probe",
-                                       "fp8 gemm producer", "fp8 gemm mma", "fp8 gemm epilogue"};
+                                       "fp8 gemm producer", "fp8 gemm mma", "fp8 gemm epilogue",
+                                       "fp8 gemm scales"};
   thread_local std::string out;
   out.clear();
   for (int b = 0; b < static_cast<int>(sizeof(kNames) / sizeof(kNames[0])); ++b)
