@@ -108,8 +108,8 @@ template <bool PAIR>
 struct Tail {
   uint64_t full[Cfg<PAIR>::STAGES];    // the stage is loaded (pair: the leader's, for both CTAs)
   uint64_t empty[Cfg<PAIR>::STAGES];   // both halves' MMAs have read it
-  uint64_t tfull[2][2];                // [half][buffer] accumulator ready
-  uint64_t tempty[2][2];               // its readers are done (pair: the leader's, for both CTAs)
+  alignas(16) uint64_t tfull[2][2];    // [half][buffer] accumulator ready
+  alignas(16) uint64_t tempty[2][2];                // its readers are done (pair: the leader's, for both CTAs)
   uint64_t xfull[2];        // gated: every epilogue warp has written its amax[tile parity]
   uint64_t sfull[2];        // a group of scales is in place
   uint64_t sempty[2];       // every epilogue warp is done with it
@@ -143,23 +143,25 @@ __device__ __forceinline__ uint32_t map_to_rank0(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
   return r;
 }
-// An arrival where `on` holds, as a predicated instruction instead of a branch.
-__device__ __forceinline__ void arrive_if(bool on, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(static_cast<uint32_t>(on))
-      : "memory");
-}
-// The same on a barrier of the pair's leader.  What it hands over are TMEM
-// columns that tcgen05.wait::ld has seen read, no memory: a release at cluster
-// scope would flush this thread's accesses, 1300 cycles in the epilogue's loop.
-__device__ __forceinline__ void arrive_if_cluster(bool on, uint32_t cluster_addr) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
-      "r"(static_cast<uint32_t>(on))
-      : "memory");
+// An arrival where `on` holds, as a predicated instruction instead of a
+// branch; of a pair on the leader's barrier (a cluster address).  What that
+// hands over are TMEM columns that tcgen05.wait::ld has seen read, no memory:
+// a release at cluster scope would flush this thread's accesses, 1300 cycles
+// in the epilogue's loop.
+template <bool CLUSTER>
+__device__ __forceinline__ void arrive_if(bool on, uint32_t bar) {
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(on))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(on))
+        : "memory");
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs, fp32 accumulator.
@@ -241,21 +243,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Waits for the TMEM loads issued so far; a and b are what they filled, so
-// that no use of them moves ahead of the wait.
-__device__ __forceinline__ void tmem_wait(uint32_t (&a)[32], uint32_t (&b)[32]) {
-#define V8(v, i) \
-  "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), \
-      "+r"(v[i + 6]), "+r"(v[i + 7])
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; i += 8) {    // (an asm statement takes 30 operands, "+r" counting twice)
-    asm volatile("" : V8(a, i));
-    asm volatile("" : V8(b, i));
-  }
-#undef V8
-}
-
 // Four rows of A (128 columns from c0) into 512 contiguous bytes with the
 // swizzle of a tiled load (the map's box is 128 x 1).
 __device__ __forceinline__ void tma_gather4(const CUtensorMap* map, uint64_t* bar, void* dst, int c0,
@@ -277,10 +264,12 @@ __device__ __forceinline__ f32x2 both(float s) {
   asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
   return r;
 }
+// (volatile: x and y come from a TMEM load, and no use of them may move ahead
+// of the wait for it)
 __device__ __forceinline__ void fma2(f32x2& acc, uint32_t x, uint32_t y, f32x2 s) {
-  f32x2 v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(x), "r"(y));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+  asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+               : "+l"(acc)
+               : "r"(x), "r"(y), "l"(s));
 }
 __device__ __forceinline__ float2 unpack(f32x2 v) {
   float2 r;
@@ -323,11 +312,17 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsig
   mbar_wait(bar, parity, &dummy, err, site);
 }
 
-// Bounded wait, suspended in the instruction where it can be.
+// Bounded wait with a short loop first.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* err,
                                      unsigned int site) {
-  if (__builtin_expect(mbar_try_wait_long(bar, parity), 1)) return true;
+  if (__builtin_expect(mbar_try_loop(smem_u32(bar), parity), 1)) return true;
   return mbar_wait(bar, parity, abort, err, site);
+}
+// The same for a converged warp, with the same result in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, volatile int* abort,
+                                          unsigned int* err, unsigned int site) {
+  if (__builtin_expect(mbar_try_loop_warp(smem_u32(bar), parity, lane), 1)) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, site));
 }
 
 // True in one lane of the (converged) warp, always the same one.
@@ -447,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 4; ++i)              // past the last row: that row again
           tok[i] = __ldg(p.perm + tl.row0 + min(4 * lane + i, rows - 1)) / p.slots;
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!__all_sync(0xffffffffu, wait(&st->empty[stage], phase ^ 1u, abort, p.err, SITE_FP8_PRODUCER))) {
+          if (!warp_wait(&st->empty[stage], phase ^ 1u, lane, abort, p.err, SITE_FP8_PRODUCER)) {
             ok = false;
             break;
           }
@@ -471,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (box = 0; (8 << box) < min(BM, tl.rows);) ++box;
         const uint32_t tx = PAIR ? 2 * C::STAGE_BYTES : (8 << box) * BK + C::B_BYTES;
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (__builtin_expect(!wait(&st->empty[stage], phase ^ 1u, abort, p.err, SITE_FP8_PRODUCER), 0)) {
+          if (!wait(&st->empty[stage], phase ^ 1u, abort, p.err, SITE_FP8_PRODUCER)) {
             ok = false;
             break;
           }
@@ -502,6 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t da = sw128_kmajor_desc(smem_u32(sA));
       const uint64_t db = sw128_kmajor_desc(smem_u32(sB) + half * (PAIR ? 64 : 128) * BK);
       const uint32_t d0 = tmem + half * 2 * BH;
+      const uint32_t full0 = smem_u32(&st->full[0]), tempty0 = smem_u32(&st->tempty[half][0]);
       int stage = 0;
       uint32_t phase = 0, i = 0;                  // i: blocks issued so far
       bool ok = true;
@@ -509,11 +505,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int kb = 0; kb < p.num_kb; ++kb, ++i) {
           const uint32_t buf = i & 1u;
           const uint32_t tpar = ((i >> 1) & 1u) ^ 1u;
-          const bool loaded = mbar_try_wait_long(&st->full[stage], phase);
-          const bool free = mbar_try_wait_long(&st->tempty[half][buf], tpar);
-          if (__builtin_expect(!(loaded && free), 0)) {
-            if (!mbar_wait(&st->full[stage], phase, abort, p.err, SITE_FP8_MMA) ||
-                !mbar_wait(&st->tempty[half][buf], tpar, abort, p.err, SITE_FP8_MMA)) {
+          if (!mbar_try_both(full0 + 8 * stage, phase, tempty0 + 8 * buf, tpar)) {
+            if (!wait(&st->full[stage], phase, abort, p.err, SITE_FP8_MMA) ||
+                !wait(&st->tempty[half][buf], tpar, abort, p.err, SITE_FP8_MMA)) {
               ok = false;
               break;
             }
@@ -579,9 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (uint32_t g = 0; t < total; ++g) {       // g: groups stored so far
       const uint32_t buf = g & 1u;
-      if (!__all_sync(0xffffffffu, wait(&st->sempty[buf], ((g >> 1) & 1u) ^ 1u, abort, p.err,
-                                        SITE_FP8_SCALES)))
-        break;
+      if (!warp_wait(&st->sempty[buf], ((g >> 1) & 1u) ^ 1u, lane, abort, p.err, SITE_FP8_SCALES)) break;
 #pragma unroll
       for (int h = 0; h < 4; ++h)
 #pragma unroll
@@ -604,10 +596,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int quad = warp & 3;                   // TMEM lanes this warp may access
     const int half = (warp - EPI_WARP0) >> 2;
     const int r = quad * 32 + lane;              // row of this CTA's 128
-    const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 2 * BH;
-    const uint32_t freed[2] = {PAIR ? map_to_rank0(&st->tempty[half][0]) : 0u,
-                               PAIR ? map_to_rank0(&st->tempty[half][1]) : 0u};
-    uint32_t i = 0;                              // blocks read so far
+    // the buffer to read next: its columns, its barriers (8 bytes apart at
+    // multiples of 16) and the parity of its turn
+    uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 2 * BH;
+    uint32_t tfull = smem_u32(&st->tfull[half][0]);
+    uint32_t tempty = PAIR ? map_to_rank0(&st->tempty[half][0]) : smem_u32(&st->tempty[half][0]);
+    uint32_t par = 0;
     uint32_t g = 0;                              // groups of scales taken so far
     int n = 0;                                   // tiles begun before this one
     for (int t = worker; t < total; t += workers, ++n) {
@@ -619,65 +613,58 @@ __global__ void __launch_bounds__(THREADS, 1)
       f32x2 acc[2][32];                          // 64 columns of each weight block, in pairs
 #pragma unroll
       for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0ull;
-      // One block's accumulator, times a * w, onto the sums.  Branches cost
-      // this loop as much as its arithmetic: the wait's usual path has none,
-      // and one lane's arrivals are predicated instructions.
-      auto add_block = [&](uint32_t buf, uint32_t par, float a, float2 w) {
-        const uint32_t src = tb + buf * BH;
-        const bool ready = mbar_try_wait_long(&st->tfull[half][buf], par);
-        __syncwarp();
-        tc_fence_after();
-        uint32_t v0[32], v1[32];
-        // The first loads go out before the result of the wait is looked at;
-        // after a wait that had to be taken up again, they are repeated.
-        if (live) {
-          tmem_ld32(src, v0);
-          tmem_ld32(src + 32, v1);
-        }
-        const f32x2 s0 = both(a * w.x), s1 = both(a * w.y);
-        if (__builtin_expect(__any_sync(0xffffffffu, !ready), 0)) {
-          mbar_wait(&st->tfull[half][buf], par, abort, p.err, SITE_FP8_EPILOGUE);
-          __syncwarp();
-          tc_fence_after();
-          if (live) {
-            tmem_ld_wait();
-            tmem_ld32(src, v0);
-            tmem_ld32(src + 32, v1);
-          }
-        }
-        if (live) {
-          tmem_wait(v0, v1);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc[0][j], v0[2 * j], v0[2 * j + 1], s0);
-          tmem_ld32(src + 64, v0);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc[0][16 + j], v1[2 * j], v1[2 * j + 1], s0);
-          tmem_ld32(src + 96, v1);
-          tmem_wait(v0, v1);
-        }
-        // all of it is in registers: the buffer is free
-        tc_fence_before();
-        __syncwarp();
-        if constexpr (PAIR) arrive_if_cluster(lane == 0, freed[buf]);
-        else arrive_if(lane == 0, &st->tempty[half][buf]);
-        if (live) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc[1][j], v0[2 * j], v0[2 * j + 1], s1);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc[1][16 + j], v1[2 * j], v1[2 * j + 1], s1);
-        }
-      };
+      // Each block's accumulator, times a * w, onto the sums.  A scheduler has
+      // two such warps, so what counts is the length of this chain: few
+      // branches, one lane's arrivals as predicated instructions, the next
+      // block's scales read ahead, addresses that flip by one xor.
       for (int k0 = 0; k0 < p.num_kb; k0 += SCALE_KB, ++g) {
         const uint32_t sbuf = g & 1u;
-        wait(&st->sfull[sbuf], (g >> 1) & 1u, abort, p.err, SITE_FP8_EPILOGUE);
-        __syncwarp();
+        warp_wait(&st->sfull[sbuf], (g >> 1) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
         const float* sa = &st->sa[sbuf][0][r];
         const float2* sw = st->sw[sbuf];
         const int nk = min(SCALE_KB, p.num_kb - k0);
+        float a = sa[0];
+        float2 w = sw[0];
 #pragma unroll 1
-        for (int k = 0; k < nk; ++k, ++i) add_block(i & 1u, (i >> 1) & 1u, sa[k * BM], sw[k]);
+        for (int k = 0; k < nk; ++k) {
+          if (__any_sync(0xffffffffu, !mbar_try(tfull, par)))
+            warp_wait(&st->tfull[half][(src >> 7) & 1u], par, lane, abort, p.err, SITE_FP8_EPILOGUE);
+          tc_fence_after();
+          uint32_t v0[32], v1[32];
+          if (live) {
+            tmem_ld32(src, v0);
+            tmem_ld32(src + 32, v1);
+          }
+          const f32x2 s0 = both(a * w.x), s1 = both(a * w.y);
+          const int kn = min(k + 1, SCALE_KB - 1);
+          a = sa[kn * BM];
+          w = sw[kn];
+          if (live) {
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) fma2(acc[0][j], v0[2 * j], v0[2 * j + 1], s0);
+            tmem_ld32(src + 64, v0);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) fma2(acc[0][16 + j], v1[2 * j], v1[2 * j + 1], s0);
+            tmem_ld32(src + 96, v1);
+            tmem_ld_wait();
+          }
+          // all of it is in registers, of every lane: the buffer is free
+          tc_fence_before();
+          arrive_if<PAIR>(lane == 0, tempty);
+          par ^= (src >> 7) & 1u;                // after the second buffer
+          src ^= BH;
+          tfull ^= 8u;
+          tempty ^= 8u;
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) fma2(acc[1][j], v0[2 * j], v0[2 * j + 1], s1);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) fma2(acc[1][16 + j], v1[2 * j], v1[2 * j + 1], s1);
+          }
+        }
         __syncwarp();
-        arrive_if(lane == 0, &st->sempty[sbuf]);
+        arrive_if<false>(lane == 0, smem_u32(&st->sempty[sbuf]));
       }
 
       if constexpr (EPI == kSiluQuant) {
@@ -698,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // meet the other half's warps
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->xfull[parity]);
-        wait(&st->xfull[parity], (n >> 1) & 1u, abort, p.err, SITE_FP8_EPILOGUE);
+        warp_wait(&st->xfull[parity], (n >> 1) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
         m = fmaxf(st->amax[parity][0][r], st->amax[parity][1][r]);
         const float s = fp8_scale(m);
         const float inv = 1.f / s;
