@@ -189,7 +189,7 @@ def _ptr(t) -> int | None:
 
 def _dtype_code(t) -> int:
     import torch
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return F32
     if t.dtype == torch.bfloat16:
         return BF16
@@ -414,7 +414,48 @@ def _blocks(n: int) -> int:
 
 
 def _rows(t) -> int:
-    return int(t.numel() // t.shape[-1]) if t.shape[-1] else 0
+    return t.numel() // t.shape[-1] if t.shape[-1] else 0
+
+
+# The 8-bit calls take microseconds on the GPU at decode sizes, so their
+# binding is kept short: torch and the library are looked up once, and an
+# argument that is as it should be costs one comparison of each kind.
+_torch = None
+
+
+def _fast():
+    """(torch, library, current device), loading the first two when needed."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch, _lib or lib(), _torch.cuda.current_device() if _torch.cuda.is_initialized() else -1
+
+
+def _raw_stream(stream, dev: int):
+    """The cudaStream_t of a stream argument (None: the current stream of device dev)."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else _stream(None)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _want(t, shape, dtype, name, dev, required=True):
+    """Checks one tensor and returns its address (0 for None)."""
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return 0
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev >= 0:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
 def add_rmsnorm(x, weight, eps: float, residual=None, sum_out=None, out=None, out8=None,
@@ -422,21 +463,19 @@ def add_rmsnorm(x, weight, eps: float, residual=None, sum_out=None, out=None, ou
     """moe_add_rmsnorm on torch tensors.  x (..., D); weight (D,); residual,
     sum_out, out like x; out8 float8_e4m3fn like x; scales float32
     (rows, ceil(D / 128))."""
-    import torch
-    D = int(x.shape[-1])
+    torch, L, dev = _fast()
+    shape, dtype = x.shape, x.dtype
+    D = shape[-1]
     T = _rows(x)
     dt = _dtype_code(x)
-    if dt in (F32, BF16) and T > 0:
-        _expect(x, x.shape, "x")
-        _expect(weight, (D,), "weight", x.dtype)
-        _expect(residual, x.shape, "residual", x.dtype, False)
-        _expect(sum_out, x.shape, "sum_out", x.dtype, False)
-        _expect(out, x.shape, "out", x.dtype, False)
-        _expect(out8, x.shape, "out8", torch.float8_e4m3fn, False)
-        _expect(scales, (T, _blocks(D)), "scales", torch.float32, False)
-    _check(lib().moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), T, D, dt,
-                                 _ptr(sum_out), _ptr(out), _ptr(out8), _ptr(scales),
-                                 _stream(stream)))
+    ok = dt in (F32, BF16) and T > 0       # else the library says what is wrong
+    px, pw, pr, ps, po, p8, pc = (
+        _want(x, shape, dtype, "x", dev), _want(weight, (D,), dtype, "weight", dev),
+        _want(residual, shape, dtype, "residual", dev, False),
+        _want(sum_out, shape, dtype, "sum_out", dev, False), _want(out, shape, dtype, "out", dev, False),
+        _want(out8, shape, torch.float8_e4m3fn, "out8", dev, False),
+        _want(scales, (T, _blocks(D)), torch.float32, "scales", dev, False)) if ok else (None,) * 7
+    _check(L.moe_add_rmsnorm(px, pr, pw, eps, T, D, dt, ps, po, p8, pc, _raw_stream(stream, dev)))
 
 
 def quantize_fp8(x, out8, scales, block_rows: int = 1, stream=None) -> None:
@@ -444,25 +483,26 @@ def quantize_fp8(x, out8, scales, block_rows: int = 1, stream=None) -> None:
     float8_e4m3fn like x, scales float32: (..., rows, ceil(cols / 128)) with
     block_rows 1, (..., ceil(rows / 128), ceil(cols / 128)) with 128.  Give a
     gate_up weight (E, 2F, D) as its view (E, 2, F, D)."""
-    import torch
+    torch, L, dev = _fast()
     if x.dim() < 2:
         raise ValueError("x needs at least two dimensions (rows, cols)")
-    rows, cols = int(x.shape[-2]), int(x.shape[-1])
+    rows, cols = x.shape[-2], x.shape[-1]
     dt = _dtype_code(x)
+    px = p8 = pc = None
     if dt in (F32, BF16) and x.numel() > 0 and block_rows in (1, QUANT_BLOCK):
-        _expect(x, x.shape, "x")
-        _expect(out8, x.shape, "out8", torch.float8_e4m3fn)
-        _expect(scales, (*x.shape[:-2], rows if block_rows == 1 else _blocks(rows), _blocks(cols)),
-                "scales", torch.float32)
+        px = _want(x, x.shape, x.dtype, "x", dev)
+        p8 = _want(out8, x.shape, torch.float8_e4m3fn, "out8", dev)
+        pc = _want(scales, (*x.shape[:-2], rows if block_rows == 1 else _blocks(rows), _blocks(cols)),
+                   torch.float32, "scales", dev)
     mats = x.numel() // (rows * cols) if rows * cols else 0
-    _check(lib().moe_quantize_fp8(_ptr(x), dt, mats, rows, cols, int(block_rows), _ptr(out8),
-                                  _ptr(scales), _stream(stream)))
+    _check(L.moe_quantize_fp8(px, dt, mats, rows, cols, block_rows, p8, pc, _raw_stream(stream, dev)))
 
 
-def _group_opts(score, selection_bias, groups, top_groups, group_score, scale) -> GroupOpts:
+def _group_opts(score, selection_bias, groups, top_groups, group_score, scale, E, dev) -> GroupOpts:
     sc = SCORE_NAMES.get(score, 99) if isinstance(score, str) else int(score)
     gs = GROUP_NAMES.get(group_score, 99) if isinstance(group_score, str) else int(group_score)
-    return GroupOpts(sc, _ptr(selection_bias), int(groups), int(top_groups), gs, float(scale))
+    bias = _want(selection_bias, (E,), _torch.float32, "selection_bias", dev, False)
+    return GroupOpts(sc, bias or None, groups, top_groups, gs, scale)
 
 
 def select_experts(logits, K: int, norm_topk_prob: bool, selected_experts, routing_weights,
@@ -470,18 +510,17 @@ def select_experts(logits, K: int, norm_topk_prob: bool, selected_experts, routi
                    group_score="max", scale: float = 1.0, stream=None) -> None:
     """moe_select_experts on torch tensors: logits (..., E) float32,
     selected_experts int64 and routing_weights float32 of K per row."""
-    import torch
-    E = int(logits.shape[-1])
+    torch, L, dev = _fast()
+    E = logits.shape[-1]
     T = _rows(logits)
+    pl = ps = pw = None
     if T > 0 and K >= 1:
-        _expect(logits, logits.shape, "logits", torch.float32)
-        _expect(selected_experts, (T, K), "selected_experts", torch.int64)
-        _expect(routing_weights, (T, K), "routing_weights", torch.float32)
-        _expect(selection_bias, (E,), "selection_bias", torch.float32, False)
-    o = _group_opts(score, selection_bias, groups, top_groups, group_score, scale)
-    _check(lib().moe_select_experts(_ptr(logits), T, E, K, 1 if norm_topk_prob else 0,
-                                    ctypes.byref(o), _ptr(selected_experts), _ptr(routing_weights),
-                                    _stream(stream)))
+        pl = _want(logits, logits.shape, torch.float32, "logits", dev)
+        ps = _want(selected_experts, (T, K), torch.int64, "selected_experts", dev)
+        pw = _want(routing_weights, (T, K), torch.float32, "routing_weights", dev)
+    o = _group_opts(score, selection_bias, groups, top_groups, group_score, scale, E, dev)
+    _check(L.moe_select_experts(pl, T, E, K, 1 if norm_topk_prob else 0, ctypes.byref(o), ps, pw,
+                                _raw_stream(stream, dev)))
 
 
 def route_groups(x, router, K: int, norm_topk_prob: bool, router_logits, selected_experts,
@@ -490,47 +529,47 @@ def route_groups(x, router, K: int, norm_topk_prob: bool, router_logits, selecte
                  stream=None) -> None:
     """moe_route_groups on torch tensors: the router's product, then
     :func:`select_experts`; router_logits (T, E) float32 is written."""
-    import torch
-    D = int(x.shape[-1])
+    torch, L, dev = _fast()
+    D = x.shape[-1]
     T = _rows(x)
-    E = int(router.shape[0])
+    E = router.shape[0]
     dt = _dtype_code(x)
+    px = pr = pb = pl = ps = pw = None
     if dt in (F32, BF16) and T > 0 and K >= 1:
-        _expect(x, x.shape, "x")
-        _expect(router, (E, D), "router", x.dtype)
-        _expect(router_bias, (E,), "router_bias", torch.float32, False)
-        _expect(router_logits, (T, E), "router_logits", torch.float32)
-        _expect(selected_experts, (T, K), "selected_experts", torch.int64)
-        _expect(routing_weights, (T, K), "routing_weights", torch.float32)
-        _expect(selection_bias, (E,), "selection_bias", torch.float32, False)
-    o = _group_opts(score, selection_bias, groups, top_groups, group_score, scale)
-    _check(lib().moe_route_groups(_ptr(x), _ptr(router), _ptr(router_bias), T, D, E, K,
-                                  1 if norm_topk_prob else 0, dt, ctypes.byref(o),
-                                  _ptr(router_logits), _ptr(selected_experts),
-                                  _ptr(routing_weights), _stream(stream)))
+        px = _want(x, x.shape, x.dtype, "x", dev)
+        pr = _want(router, (E, D), x.dtype, "router", dev)
+        pb = _want(router_bias, (E,), torch.float32, "router_bias", dev, False) or None
+        pl = _want(router_logits, (T, E), torch.float32, "router_logits", dev)
+        ps = _want(selected_experts, (T, K), torch.int64, "selected_experts", dev)
+        pw = _want(routing_weights, (T, K), torch.float32, "routing_weights", dev)
+    o = _group_opts(score, selection_bias, groups, top_groups, group_score, scale, E, dev)
+    _check(L.moe_route_groups(px, pr, pb, T, D, E, K, 1 if norm_topk_prob else 0, dt, ctypes.byref(o),
+                              pl, ps, pw, _raw_stream(stream, dev)))
 
 
 def gemm_fp8(a, a_scales, w, w_scales, out, offsets=None, stream=None) -> None:
     """moe_gemm_fp8 on torch tensors: a (M, K), w (E, N, K) or (N, K)
     float8_e4m3fn; scales float32; offsets (E + 1,) int32; out (M, N)
     bfloat16 or float32."""
-    import torch
+    torch, L, dev = _fast()
     if a.dim() != 2 or w.dim() not in (2, 3):
         raise ValueError("a must be (M, K), w (E, N, K) or (N, K)")
-    M, K = int(a.shape[0]), int(a.shape[1])
-    N = int(w.shape[-2])
-    E = int(w.shape[0]) if w.dim() == 3 else 1
+    M, K = a.shape
+    ws = w.shape
+    N = ws[-2]
+    E = ws[0] if len(ws) == 3 else 1
     dt = _dtype_code(out)
+    pa = pc = pw = pv = pf = po = None
     if dt in (F32, BF16) and M > 0 and N > 0 and K > 0 and E > 0:
-        f8 = torch.float8_e4m3fn
-        _expect(a, a.shape, "a", f8)
-        _expect(a_scales, (M, _blocks(K)), "a_scales", torch.float32)
-        _expect(w, (*w.shape[:-1], K), "w", f8)
-        _expect(w_scales, (*w.shape[:-2], _blocks(N), _blocks(K)), "w_scales", torch.float32)
-        _expect(offsets, (E + 1,), "offsets", torch.int32, False)
-        _expect(out, (M, N), "out")
-    _check(lib().moe_gemm_fp8(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), E, M,
-                              N, K, _ptr(out), dt, _stream(stream)))
+        f8, f32 = torch.float8_e4m3fn, torch.float32
+        kb = _blocks(K)
+        pa = _want(a, (M, K), f8, "a", dev)
+        pc = _want(a_scales, (M, kb), f32, "a_scales", dev)
+        pw = _want(w, (*ws[:-1], K), f8, "w", dev)
+        pv = _want(w_scales, (*ws[:-2], _blocks(N), kb), f32, "w_scales", dev)
+        pf = _want(offsets, (E + 1,), torch.int32, "offsets", dev, False) or None
+        po = _want(out, (M, N), out.dtype, "out", dev)
+    _check(L.moe_gemm_fp8(pa, pc, pw, pv, pf, E, M, N, K, po, dt, _raw_stream(stream, dev)))
 
 
 def experts_workspace_size_fp8(T: int, D: int, F: int, E: int, K: int) -> int:
@@ -544,28 +583,27 @@ def experts_forward_fp8(x, x_scales, selected_experts, routing_weights, gate_up_
     (T, ceil(D / 128)), gate_up_scales (E, 2, ceil(F / 128), ceil(D / 128)),
     down_scales (E, ceil(D / 128), ceil(F / 128)) float32; selected_experts
     (T, K) int64, routing_weights (T, K) float32; out bfloat16 like x."""
-    import torch
-    D = int(x.shape[-1])
+    torch, L, dev = _fast()
+    D = x.shape[-1]
     T = _rows(x)
-    E, F = int(down_proj.shape[0]), int(down_proj.shape[-1])
-    K = int(selected_experts.shape[-1])
+    E, F = down_proj.shape[0], down_proj.shape[-1]
+    K = selected_experts.shape[-1]
+    ptrs, ws_bytes, pws = (None,) * 9, 0, None
     if T > 0 and E > 0 and F > 0 and K > 0:
         f8, f32 = torch.float8_e4m3fn, torch.float32
         db, fb = _blocks(D), _blocks(F)
-        _expect(x, x.shape, "x", f8)
-        _expect(x_scales, (T, db), "x_scales", f32)
-        _expect(selected_experts, (T, K), "selected_experts", torch.int64)
-        _expect(routing_weights, (T, K), "routing_weights", f32)
-        _expect(gate_up_proj, (E, 2 * F, D), "gate_up_proj", f8)
-        _expect(gate_up_scales, (E, 2, fb, db), "gate_up_scales", f32)
-        _expect(down_proj, (E, D, F), "down_proj", f8)
-        _expect(down_scales, (E, db, fb), "down_scales", f32)
-        _expect(out, x.shape, "out", torch.bfloat16)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().moe_experts_forward_fp8(
-        _ptr(x), _ptr(x_scales), _ptr(selected_experts), _ptr(routing_weights), _ptr(gate_up_proj),
-        _ptr(gate_up_scales), _ptr(down_proj), _ptr(down_scales), _ptr(out), T, D, F, E, K,
-        _ptr(workspace), ws_bytes, _stream(stream)))
+        ptrs = (_want(x, x.shape, f8, "x", dev), _want(x_scales, (T, db), f32, "x_scales", dev),
+                _want(selected_experts, (T, K), torch.int64, "selected_experts", dev),
+                _want(routing_weights, (T, K), f32, "routing_weights", dev),
+                _want(gate_up_proj, (E, 2 * F, D), f8, "gate_up_proj", dev),
+                _want(gate_up_scales, (E, 2, fb, db), f32, "gate_up_scales", dev),
+                _want(down_proj, (E, D, F), f8, "down_proj", dev),
+                _want(down_scales, (E, db, fb), f32, "down_scales", dev),
+                _want(out, x.shape, torch.bfloat16, "out", dev))
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        pws = _want(workspace, workspace.shape, workspace.dtype, "workspace", dev)
+    _check(L.moe_experts_forward_fp8(*ptrs, T, D, F, E, K, pws, ws_bytes, _raw_stream(stream, dev)))
 
 
 GEMM_AUTO, GEMM_1SM, GEMM_2SM = 0, 1, 2
