@@ -61,7 +61,6 @@ constexpr int BM = 128;                        // rows per CTA
 constexpr int BK = 128;                        // bytes = e4m3 values = one scale block
 constexpr int BN = 256;                        // weight rows per tile
 constexpr int BH = 128;                        // columns of a half
-constexpr int A_BYTES = BM * BK;               // 16 KB
 constexpr int EPI_WARP0 = 4;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
@@ -71,13 +70,19 @@ constexpr int kBoxes = 5;                      // A boxes of 8, 16, 32, 64 and 1
 constexpr int kRowGroup = 16;                  // row blocks that share a pass over the weights
 
 constexpr long long kPairRows = 192;           // rows per expert from which pairs run
+constexpr long long kFewRows = 32;             // and up to which the 32-row form does
 
-template <bool PAIR>
+// kOne: a CTA, 128 rows.  kPair: a CTA pair, 256 rows.  kFew: a CTA, 32 rows.
+enum { kOne = 0, kPair = 1, kFew = 2 };
+
+template <int MODE>
 struct Cfg {
-  static constexpr int STAGES = PAIR ? 6 : 4;
-  static constexpr int B_BYTES = (PAIR ? BN / 2 : BN) * BK;
+  static constexpr int TILE_M = MODE == kPair ? 2 * BM : MODE == kFew ? 32 : BM;
+  static constexpr int STAGES = MODE == kPair ? 6 : MODE == kFew ? 5 : 4;
+  static constexpr int A_BYTES = (MODE == kFew ? TILE_M : BM) * BK;
+  static constexpr int B_BYTES = (MODE == kPair ? BN / 2 : BN) * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int TILE_M = PAIR ? 2 * BM : BM;
+  static constexpr int QUADS = MODE == kFew ? 1 : 4;   // groups of 32 TMEM lanes with rows
 };
 
 enum { kOutBf16 = 0, kOutF32 = 1, kSiluQuant = 2 };
@@ -97,6 +102,7 @@ struct Params {
   int w_rows;            // weight rows per expert
   int w_blocks;          // scale rows per expert
   int up_row, up_block;  // first up row and scale row of an expert (gated)
+  int split;             // kFew: CTAs of a cluster that share a tile's blocks
   const float* sa;       // (rows, num_kb)
   const float* sw;       // (E, w_blocks, num_kb)
   void* out;             // (M, n_out) bf16, fp32 or e4m3
@@ -104,10 +110,10 @@ struct Params {
   unsigned int* err;
 };
 
-template <bool PAIR>
+template <int MODE>
 struct Tail {
-  uint64_t full[Cfg<PAIR>::STAGES];    // the stage is loaded (pair: the leader's, for both CTAs)
-  uint64_t empty[Cfg<PAIR>::STAGES];   // both halves' MMAs have read it
+  uint64_t full[Cfg<MODE>::STAGES];    // the stage is loaded (pair: the leader's, for both CTAs)
+  uint64_t empty[Cfg<MODE>::STAGES];   // both halves' MMAs have read it
   alignas(16) uint64_t tfull[2][2];    // [half][buffer] accumulator ready
   alignas(16) uint64_t tempty[2][2];                // its readers are done (pair: the leader's, for both CTAs)
   uint64_t xfull[2];        // gated: every epilogue warp has written its amax[tile parity]
@@ -124,11 +130,20 @@ struct Tail {
   alignas(16) float2 sw[2][SCALE_KB];   // of the first and the second 128 weight rows
 };
 
-template <bool PAIR>
+template <int MODE>
 constexpr size_t smem_bytes() {
-  return 1024 + Cfg<PAIR>::STAGES * Cfg<PAIR>::STAGE_BYTES + sizeof(Tail<PAIR>);
+  return 1024 + Cfg<MODE>::STAGES * Cfg<MODE>::STAGE_BYTES + sizeof(Tail<MODE>);
 }
-static_assert(smem_bytes<false>() <= 227 * 1024 && smem_bytes<true>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<kOne>() <= 227 * 1024 && smem_bytes<kPair>() <= 227 * 1024 &&
+              smem_bytes<kFew>() <= 227 * 1024, "shared memory");
+// Split blocks: a CTA's sums of its share, a row of 256 columns after the
+// other, in the ring that its loads have left; 16 bytes more per row keep
+// row-per-lane accesses free of bank conflicts.
+constexpr int kPartStride = BN + 4;
+static_assert(Cfg<kFew>::TILE_M * kPartStride * 4 <= Cfg<kFew>::STAGES * Cfg<kFew>::STAGE_BYTES, "partials");
+// An M = 128 MMA of kFew reads past the stage's 32 rows into what follows in
+// shared memory (rows that are never looked at): it has to be there.
+static_assert(Cfg<kFew>::STAGES * Cfg<kFew>::B_BYTES >= BM * BK, "A reads stay inside the ring");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -137,6 +152,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Four floats at the shared-memory address `addr` of the cluster's CTA `rank`.
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, int rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ uint32_t map_to_rank0(const void* p) {
   uint32_t r;
@@ -336,25 +362,31 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-template <int EPI, bool PAIR>
+template <int EPI, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ CUtensorMap tmB,
                     const Params p) {
-  using C = Cfg<PAIR>;
-  constexpr int STAGES = C::STAGES;
+  using C = Cfg<MODE>;
+  constexpr bool PAIR = MODE == kPair;
+  constexpr int STAGES = C::STAGES, A_BYTES = C::A_BYTES;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned by its address in the shared window: the same offset in
   // both CTAs of a pair
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * A_BYTES;
-  Tail<PAIR>* st = reinterpret_cast<Tail<PAIR>*>(smem + STAGES * C::STAGE_BYTES);
+  Tail<MODE>* st = reinterpret_cast<Tail<MODE>*>(smem + STAGES * C::STAGE_BYTES);
 
   constexpr int BN_OUT = EPI == kSiluQuant ? 128 : 256;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
-  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x;         // takes tiles worker, worker + workers, ...
-  const int workers = PAIR ? gridDim.x >> 1 : gridDim.x;
+  // this CTA (or pair, or cluster) takes tiles worker, worker + workers, ...;
+  // with split blocks one tile only: the grid covers every possible one
+  const int split = MODE == kFew ? p.split : 1;
+  const int share = MODE == kFew && split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x / split;
+  const int workers = PAIR ? gridDim.x >> 1 : split > 1 ? 1 << 30 : gridDim.x;
+  const int kb_lo = share * p.num_kb / split, kb_hi = (share + 1) * p.num_kb / split;
   const int E = p.E;
   const int n_tiles = (p.n_out + BN_OUT - 1) / BN_OUT;
 
@@ -366,11 +398,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int a = 0; a < 2; ++a) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&st->tfull[a][b], 1);
-        mbar_init(&st->tempty[a][b], PAIR ? EPI_WARPS : EPI_WARPS / 2);
+        mbar_init(&st->tempty[a][b], (PAIR ? 2 : 1) * C::QUADS);
       }
-      mbar_init(&st->xfull[a], EPI_WARPS);
+      mbar_init(&st->xfull[a], 2 * C::QUADS);
       mbar_init(&st->sfull[a], 1);
-      mbar_init(&st->sempty[a], EPI_WARPS);
+      mbar_init(&st->sempty[a], 2 * C::QUADS);
       mbar_init(&st->mma_done[a], 1);
     }
     st->abort = 0;
@@ -432,16 +464,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     };
     bool ok = true;
-    if (!PAIR && p.gather) {
+    if (MODE == kFew && p.gather) {
       for (int t = worker; t < total && ok; t += workers) {
         const Tile tl = tile_of(t);
-        const int rows = min(BM, tl.rows);
+        const int rows = min(C::TILE_M, tl.rows);
         const int fetchers = (rows + 3) >> 2;    // lanes with rows, four each
         int tok[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)              // past the last row: that row again
           tok[i] = __ldg(p.perm + tl.row0 + min(4 * lane + i, rows - 1)) / p.slots;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb) {
           if (!warp_wait(&st->empty[stage], phase ^ 1u, lane, abort, p.err, SITE_FP8_PRODUCER)) {
             ok = false;
             break;
@@ -463,9 +495,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const Tile tl = tile_of(t);
         int box = kBoxes - 1;
         if constexpr (!PAIR)
-          for (box = 0; (8 << box) < min(BM, tl.rows);) ++box;
+          for (box = 0; (8 << box) < min(C::TILE_M, tl.rows);) ++box;
         const uint32_t tx = PAIR ? 2 * C::STAGE_BYTES : (8 << box) * BK + C::B_BYTES;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb) {
           if (!wait(&st->empty[stage], phase ^ 1u, abort, p.err, SITE_FP8_PRODUCER)) {
             ok = false;
             break;
@@ -492,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // operands of tcgen05.mma are uniform (with `lane == 0` an issue takes
     // three times as long).
     const int half = warp - 1;
-    constexpr uint32_t idesc = idesc_e4m3_f32(C::TILE_M, BH);
+    constexpr uint32_t idesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BH);
     if (rank == 0 && elect_one()) {
       const uint64_t da = sw128_kmajor_desc(smem_u32(sA));
       const uint64_t db = sw128_kmajor_desc(smem_u32(sB) + half * (PAIR ? 64 : 128) * BK);
@@ -502,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t phase = 0, i = 0;                  // i: blocks issued so far
       bool ok = true;
       for (int t = worker; t < total && ok; t += workers) {
-        for (int kb = 0; kb < p.num_kb; ++kb, ++i) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb, ++i) {
           const uint32_t buf = i & 1u;
           const uint32_t tpar = ((i >> 1) & 1u) ^ 1u;
           if (!mbar_try_both(full0 + 8 * stage, phase, tempty0 + 8 * buf, tpar)) {
@@ -530,18 +562,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     // -------------------------------------------------------- scale loader
     // A group's loads are issued before the wait for its place in shared
     // memory, so that their latency passes while the group before is used.
-    const bool vec = (p.num_kb & 3) == 0;        // a row's scales start at 16 bytes
+    const bool vec = ((p.num_kb | kb_lo) & 3) == 0;   // a row's scales start at 16 bytes
     const int k = lane & 7;                      // lanes 0..7: the first weight block's, 8..15: the second's
     const float* sw = nullptr;
-    const float* sa[4];
-    float va[4][SCALE_KB], vw = 0.f;
+    const float* sa[C::QUADS];
+    float va[C::QUADS][SCALE_KB], vw = 0.f;
     auto point = [&](int t) {                    // at tile t
       const Tile tl = tile_of(t);
       const int b0 = EPI == kSiluQuant ? tl.n_blk : 2 * tl.n_blk;
       const int b1 = EPI == kSiluQuant ? p.up_block + tl.n_blk : min(b0 + 1, p.w_blocks - 1);
       sw = p.sw + (static_cast<size_t>(tl.e) * p.w_blocks + (lane & 8 ? b1 : b0)) * p.num_kb;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {              // past the last row: that row again
+      for (int h = 0; h < C::QUADS; ++h) {       // past the last row: that row again
         const int grow = tl.row0 + min(static_cast<int>(rank) * BM + h * 32 + lane, tl.rows - 1);
         sa[h] = p.sa + static_cast<size_t>(p.perm ? __ldg(p.perm + grow) / p.slots : grow) * p.num_kb;
       }
@@ -549,7 +581,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto fetch = [&](int k0) {                   // past the last block: that block again
       if (vec) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < C::QUADS; ++h)
 #pragma unroll
           for (int q = 0; q < SCALE_KB / 4; ++q) {
             const float4 v = __ldg(reinterpret_cast<const float4*>(sa[h] + min(k0 + 4 * q, p.num_kb - 4)));
@@ -560,30 +592,30 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
       } else {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < C::QUADS; ++h)
 #pragma unroll
           for (int q = 0; q < SCALE_KB; ++q) va[h][q] = __ldg(sa[h] + min(k0 + q, p.num_kb - 1));
       }
       vw = __ldg(sw + min(k0 + k, p.num_kb - 1));
     };
-    int t = worker, k0 = 0;
+    int t = worker, k0 = kb_lo;
     if (t < total) {
       point(t);
-      fetch(0);
+      fetch(k0);
     }
     for (uint32_t g = 0; t < total; ++g) {       // g: groups stored so far
       const uint32_t buf = g & 1u;
       if (!warp_wait(&st->sempty[buf], ((g >> 1) & 1u) ^ 1u, lane, abort, p.err, SITE_FP8_SCALES)) break;
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
+      for (int h = 0; h < C::QUADS; ++h)
 #pragma unroll
         for (int q = 0; q < SCALE_KB; ++q) st->sa[buf][q][h * 32 + lane] = va[h][q];
       if (lane < 16) (lane & 8 ? st->sw[buf][k].y : st->sw[buf][k].x) = vw;
       __syncwarp();
       if (lane == 0) mbar_arrive(&st->sfull[buf]);
       k0 += SCALE_KB;
-      if (k0 >= p.num_kb) {
-        k0 = 0;
+      if (k0 >= kb_hi) {
+        k0 = kb_lo;
         t += workers;
         if (t < total) point(t);
       }
@@ -604,9 +636,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t par = 0;
     uint32_t g = 0;                              // groups of scales taken so far
     int n = 0;                                   // tiles begun before this one
-    for (int t = worker; t < total; t += workers, ++n) {
+    for (int t = quad < C::QUADS ? worker : total; t < total; t += workers, ++n) {
       const Tile tl = tile_of(t);
-      const int rows = tl.rows - static_cast<int>(rank) * BM;
+      const int rows = min(tl.rows - static_cast<int>(rank) * BM, MODE == kFew ? C::TILE_M : BM);
       const bool live = quad * 32 < rows;        // warp-uniform
       const bool rvalid = r < rows;
       const int grow = tl.row0 + static_cast<int>(rank) * BM + (rvalid ? r : 0);
@@ -617,12 +649,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       // two such warps, so what counts is the length of this chain: few
       // branches, one lane's arrivals as predicated instructions, the next
       // block's scales read ahead, addresses that flip by one xor.
-      for (int k0 = 0; k0 < p.num_kb; k0 += SCALE_KB, ++g) {
+      for (int k0 = kb_lo; k0 < kb_hi; k0 += SCALE_KB, ++g) {
         const uint32_t sbuf = g & 1u;
         warp_wait(&st->sfull[sbuf], (g >> 1) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
         const float* sa = &st->sa[sbuf][0][r];
         const float2* sw = st->sw[sbuf];
-        const int nk = min(SCALE_KB, p.num_kb - k0);
+        const int nk = min(SCALE_KB, kb_hi - k0);
         float a = sa[0];
         float2 w = sw[0];
 #pragma unroll 1
@@ -667,6 +699,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         arrive_if<false>(lane == 0, smem_u32(&st->sempty[sbuf]));
       }
 
+      if (split > 1) {
+        // this CTA's share of the sums into the ring, once both halves' MMAs
+        // have read their last block there
+        const int last = kb_hi - kb_lo - 1;
+        warp_wait(&st->empty[last % STAGES], (last / STAGES) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
+        if (rvalid) {
+          float* dst = reinterpret_cast<float*>(smem) + r * kPartStride + half * 64;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 x = unpack(acc[c][2 * j]), y = unpack(acc[c][2 * j + 1]);
+              *reinterpret_cast<float4*>(dst + c * 128 + 4 * j) = make_float4(x.x, x.y, y.x, y.y);
+            }
+        }
+        continue;
+      }
       if constexpr (EPI == kSiluQuant) {
         // columns [half * 64, half * 64 + 64) of the tile's 128
         const int parity = n & 1;
@@ -740,6 +789,61 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
+  if constexpr (MODE == kFew) {
+    if (split > 1) {
+      // Every CTA of the cluster adds the shares of some of the rows, in rank
+      // order, and finishes them: a warp per row, a lane four columns of each
+      // weight block.
+      cluster_sync_all();
+      if (warp >= EPI_WARP0 && worker < total) {
+        const Tile tl = tile_of(worker);
+        const int rows = min(C::TILE_M, tl.rows);
+        for (int r = share + (warp - EPI_WARP0) * split; r < rows; r += EPI_WARPS * split) {
+          float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+          const uint32_t at = smem_u32(smem) + (r * kPartStride + 4 * lane) * 4;
+          for (int q = 0; q < split; ++q) {
+            const float4 x = ld_cluster(at, q), y = ld_cluster(at + 512, q);
+            s0.x += x.x; s0.y += x.y; s0.z += x.z; s0.w += x.w;
+            s1.x += y.x; s1.y += y.y; s1.z += y.z; s1.w += y.w;
+          }
+          const size_t grow = static_cast<size_t>(tl.row0 + r) * p.n_out;
+          if constexpr (EPI == kSiluQuant) {
+            const int col = tl.n_blk * 128 + 4 * lane;
+            const bool in = col < p.n_out;       // n_out is a multiple of 16
+            float4 h;
+            h.x = in ? silu_bf16_epilogue(s0.x) * s1.x : 0.f;
+            h.y = in ? silu_bf16_epilogue(s0.y) * s1.y : 0.f;
+            h.z = in ? silu_bf16_epilogue(s0.z) * s1.z : 0.f;
+            h.w = in ? silu_bf16_epilogue(s0.w) * s1.w : 0.f;
+            const float s = fp8_scale(warp_max(fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)))));
+            const float inv = 1.f / s;
+            if (in)
+              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + grow + col) =
+                  fp8_pack4(h.x * inv, h.y * inv, h.z * inv, h.w * inv);
+            if (lane == 0)
+              p.out_scales[static_cast<size_t>(tl.row0 + r) * ((p.n_out + 127) / 128) + tl.n_blk] = s;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int col = tl.n_blk * 256 + c * 128 + 4 * lane;
+              const float4 v = c ? s1 : s0;
+              if (col >= p.n_out) continue;      // n_out is a multiple of 8
+              if constexpr (EPI == kOutBf16) {
+                uint2 w;
+                reinterpret_cast<__nv_bfloat162*>(&w)[0] = __floats2bfloat162_rn(v.x, v.y);
+                reinterpret_cast<__nv_bfloat162*>(&w)[1] = __floats2bfloat162_rn(v.z, v.w);
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + grow + col) = w;
+              } else {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + grow + col) = v;
+              }
+            }
+          }
+        }
+      }
+      cluster_sync_all();                      // no CTA leaves while its share may be read
+    }
+  }
+
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();      // neither CTA frees TMEM while its peer may still use it
@@ -785,8 +889,9 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
 
 // Workers (CTAs or pairs) that the device runs at once; sets the kernel's
 // shared-memory opt-in on the way.  Asked once per device and kernel.
-template <int EPI, bool PAIR>
+template <int EPI, int MODE>
 cudaError_t resident_workers(int* out) {
+  constexpr bool PAIR = MODE == kPair;
   static std::mutex mu;
   static int known[64] = {};
   int dev = 0;
@@ -797,8 +902,8 @@ cudaError_t resident_workers(int* out) {
     *out = known[dev];
     return cudaSuccess;
   }
-  constexpr int bytes = static_cast<int>(smem_bytes<PAIR>());
-  err = cudaFuncSetAttribute(gemm_fp8_kernel<EPI, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int bytes = static_cast<int>(smem_bytes<MODE>());
+  err = cudaFuncSetAttribute(gemm_fp8_kernel<EPI, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (err != cudaSuccess) return err;
   int n = PAIR ? num_sms() / 2 : num_sms();
   if constexpr (PAIR) {
@@ -815,7 +920,7 @@ cudaError_t resident_workers(int* out) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int fit = 0;
-    if (cudaOccupancyMaxActiveClusters(&fit, gemm_fp8_kernel<EPI, PAIR>, &cfg) == cudaSuccess && fit > 0)
+    if (cudaOccupancyMaxActiveClusters(&fit, gemm_fp8_kernel<EPI, MODE>, &cfg) == cudaSuccess && fit > 0)
       n = fit < n ? fit : n;
     else
       cudaGetLastError();              // the query is advisory
@@ -825,25 +930,46 @@ cudaError_t resident_workers(int* out) {
   return cudaSuccess;
 }
 
-template <int EPI, bool PAIR>
-cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, const Params& p, cudaStream_t s) {
+template <int EPI, int MODE>
+cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, Params p, cudaStream_t s) {
   int workers = 0;
-  const cudaError_t err = resident_workers<EPI, PAIR>(&workers);
+  const cudaError_t err = resident_workers<EPI, MODE>(&workers);
   if (err != cudaSuccess) return err;
   const int bn_out = EPI == kSiluQuant ? 128 : 256;
   const long long n_tiles = (p.n_out + bn_out - 1) / bn_out;
-  // A bound on the tiles; with at most one row block per expert on average
-  // (weight streaming) those of one block per expert.  The grid is then sized
-  // so that every worker takes the same number of tiles.
-  constexpr int tile_m = Cfg<PAIR>::TILE_M;
+  constexpr int tile_m = Cfg<MODE>::TILE_M;
   const long long touched = p.M < p.E ? p.M : p.E;
-  long long tiles = (static_cast<long long>(p.M) / tile_m + touched) * n_tiles;
+  const long long bound = p.M <= tile_m ? touched * n_tiles
+                                        : (static_cast<long long>(p.M) / tile_m + touched) * n_tiles;
+  if (MODE == kPair) {
+    const int pairs = static_cast<int>(bound < workers ? bound : workers);
+    return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(2 * pairs), dim3(THREADS), smem_bytes<MODE>(), s, false,
+                    2, a, b, p);
+  }
+  // At most half as many tiles as SMs: a cluster shares each one's blocks, as
+  // long as every CTA keeps four.
+  p.split = 1;
+  if (MODE == kFew)
+    while (p.split < 8 && bound * p.split * 2 <= workers && p.num_kb >= 8 * p.split) p.split *= 2;
+  if (p.split > 1)
+    return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(static_cast<unsigned>(bound * p.split)), dim3(THREADS),
+                    smem_bytes<MODE>(), s, false, p.split, a, b, p);
+  // With at most one row block per expert on average (weight streaming), size
+  // the grid so that every CTA takes the same number of tiles.
+  long long tiles = bound;
   if (p.M <= static_cast<long long>(tile_m) * p.E) tiles = touched * n_tiles;
   const long long waves = (tiles + workers - 1) / workers;
-  int grid = static_cast<int>((tiles + waves - 1) / waves);
-  if (PAIR) grid = 2 * static_cast<int>(tiles < workers ? tiles : workers);
-  return launch_k(gemm_fp8_kernel<EPI, PAIR>, dim3(grid), dim3(THREADS), smem_bytes<PAIR>(), s, false,
-                  PAIR ? 2 : 1, a, b, p);
+  const int grid = static_cast<int>((tiles + waves - 1) / waves);
+  return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(grid), dim3(THREADS), smem_bytes<MODE>(), s, false, 1, a,
+                  b, p);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const GemmFp8Args& g, const AMaps& a, const CUtensorMap& b, const Params& p,
+                        cudaStream_t s) {
+  if (g.q_scales) return launch_epi<kSiluQuant, MODE>(a, b, p, s);
+  if (g.out_f32) return launch_epi<kOutF32, MODE>(a, b, p, s);
+  return launch_epi<kOutBf16, MODE>(a, b, p, s);
 }
 
 }  // namespace
@@ -869,7 +995,8 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   p.out = g.out;
   p.out_scales = g.q_scales;
   p.err = g.err;
-  const bool pair = !g.gather && g.M >= kPairRows * g.E;
+  // by the rows of an expert, on average
+  const int mode = g.M <= kFewRows * g.E ? kFew : !g.gather && g.M >= kPairRows * g.E ? kPair : kOne;
   AMaps ma;
   CUtensorMap mb;
   for (int i = 0; i < kBoxes; ++i)
@@ -877,16 +1004,11 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
                   g.gather ? 1u : 8u << i))
       return cudaErrorInvalidValue;
   if (!make_map(&mb, g.w, static_cast<uint64_t>(g.E) * p.w_rows, static_cast<uint64_t>(g.K),
-                pair ? 128u : 64u))
+                mode == kPair ? 128u : 64u))
     return cudaErrorInvalidValue;
-  if (pair) {
-    if (gated) return launch_epi<kSiluQuant, true>(ma, mb, p, s);
-    if (g.out_f32) return launch_epi<kOutF32, true>(ma, mb, p, s);
-    return launch_epi<kOutBf16, true>(ma, mb, p, s);
-  }
-  if (gated) return launch_epi<kSiluQuant, false>(ma, mb, p, s);
-  if (g.out_f32) return launch_epi<kOutF32, false>(ma, mb, p, s);
-  return launch_epi<kOutBf16, false>(ma, mb, p, s);
+  if (mode == kPair) return launch_mode<kPair>(g, ma, mb, p, s);
+  if (mode == kFew) return launch_mode<kFew>(g, ma, mb, p, s);
+  return launch_mode<kOne>(g, ma, mb, p, s);
 }
 
 }  // namespace moe
