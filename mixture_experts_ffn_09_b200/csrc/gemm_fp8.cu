@@ -110,13 +110,16 @@ struct Params {
   unsigned int* err;
 };
 
+constexpr int kPartStride = BN + 4;
+
 template <int MODE>
 struct Tail {
   uint64_t full[Cfg<MODE>::STAGES];    // the stage is loaded (pair: the leader's, for both CTAs)
   uint64_t empty[Cfg<MODE>::STAGES];   // both halves' MMAs have read it
   alignas(16) uint64_t tfull[2][2];    // [half][buffer] accumulator ready
   alignas(16) uint64_t tempty[2][2];                // its readers are done (pair: the leader's, for both CTAs)
-  uint64_t xfull[2];        // gated: every epilogue warp has written its amax[tile parity]
+  uint64_t xfull[2];        // kFew: the tile's sums are in part; gated, else: its amax[tile parity] is in place
+  uint64_t xempty;          // kFew: the tile's rows are finished, part is free
   uint64_t sfull[2];        // a group of scales is in place
   uint64_t sempty[2];       // every epilogue warp is done with it
   uint64_t mma_done[2];
@@ -125,8 +128,11 @@ struct Tail {
   int total_tiles;
   int tile_start[kMaxExperts + 1];
   int off[kMaxExperts + 1];
-  alignas(16) float amax[2][2][BM];     // [tile parity][half][row]
-  alignas(16) float sa[2][SCALE_KB][BM];
+  alignas(16) float amax[2][2][MODE == kFew ? 1 : BM];   // [tile parity][half][row]
+  alignas(16) float sa[2][SCALE_KB][32 * Cfg<MODE>::QUADS];
+  // kFew: the tile's sums, a row of 256 columns after the other; 16 bytes more
+  // per row keep row-per-lane accesses free of bank conflicts
+  alignas(16) float part[MODE == kFew ? 32 : 1][kPartStride];
   alignas(16) float2 sw[2][SCALE_KB];   // of the first and the second 128 weight rows
 };
 
@@ -136,11 +142,6 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<kOne>() <= 227 * 1024 && smem_bytes<kPair>() <= 227 * 1024 &&
               smem_bytes<kFew>() <= 227 * 1024, "shared memory");
-// Split blocks: a CTA's sums of its share, a row of 256 columns after the
-// other, in the ring that its loads have left; 16 bytes more per row keep
-// row-per-lane accesses free of bank conflicts.
-constexpr int kPartStride = BN + 4;
-static_assert(Cfg<kFew>::TILE_M * kPartStride * 4 <= Cfg<kFew>::STAGES * Cfg<kFew>::STAGE_BYTES, "partials");
 // An M = 128 MMA of kFew reads past the stage's 32 rows into what follows in
 // shared memory (rows that are never looked at): it has to be there.
 static_assert(Cfg<kFew>::STAGES * Cfg<kFew>::B_BYTES >= BM * BK, "A reads stay inside the ring");
@@ -362,6 +363,44 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// One row of a tile from its sums, by a warp: a lane has columns 4 * lane .. + 3
+// of the first (v0) and of the second weight block (v1).
+template <int EPI>
+__device__ __forceinline__ void finish_row(const Params& p, const Tile& tl, int r, int lane, float4 v0,
+                                           float4 v1) {
+  const size_t grow = static_cast<size_t>(tl.row0 + r) * p.n_out;
+  if constexpr (EPI == kSiluQuant) {
+    const int col = tl.n_blk * 128 + 4 * lane;
+    const bool in = col < p.n_out;               // n_out is a multiple of 16
+    float4 h;
+    h.x = in ? silu_bf16_epilogue(v0.x) * v1.x : 0.f;
+    h.y = in ? silu_bf16_epilogue(v0.y) * v1.y : 0.f;
+    h.z = in ? silu_bf16_epilogue(v0.z) * v1.z : 0.f;
+    h.w = in ? silu_bf16_epilogue(v0.w) * v1.w : 0.f;
+    const float s = fp8_scale(warp_max(fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)))));
+    const float inv = 1.f / s;
+    if (in)
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + grow + col) =
+          fp8_pack4(h.x * inv, h.y * inv, h.z * inv, h.w * inv);
+    if (lane == 0) p.out_scales[static_cast<size_t>(tl.row0 + r) * ((p.n_out + 127) / 128) + tl.n_blk] = s;
+  } else {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = tl.n_blk * 256 + c * 128 + 4 * lane;
+      const float4 v = c ? v1 : v0;
+      if (col >= p.n_out) continue;              // n_out is a multiple of 8
+      if constexpr (EPI == kOutBf16) {
+        uint2 w;
+        reinterpret_cast<__nv_bfloat162*>(&w)[0] = __floats2bfloat162_rn(v.x, v.y);
+        reinterpret_cast<__nv_bfloat162*>(&w)[1] = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + grow + col) = w;
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + grow + col) = v;
+      }
+    }
+  }
+}
+
 template <int EPI, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ AMaps tmA, const __grid_constant__ CUtensorMap tmB,
@@ -401,25 +440,64 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&st->tempty[a][b], (PAIR ? 2 : 1) * C::QUADS);
       }
       mbar_init(&st->xfull[a], 2 * C::QUADS);
+      if (a == 0) mbar_init(&st->xempty, EPI_WARPS);
       mbar_init(&st->sfull[a], 1);
       mbar_init(&st->sempty[a], 2 * C::QUADS);
       mbar_init(&st->mma_done[a], 1);
     }
     st->abort = 0;
     mbar_fence_init();
-    // offsets are device data: kept within [0, M] and in order, so that no
-    // address below depends on their being right
-    int acc = 0, at = p.offsets ? min(max(p.offsets[0], 0), p.M) : 0;
-    for (int e = 0; e < E; ++e) {
-      const int next = p.offsets ? min(max(p.offsets[e + 1], at), p.M) : p.M;
-      st->off[e] = at;
-      st->tile_start[e] = acc;
-      acc += (next - at + C::TILE_M - 1) / C::TILE_M * n_tiles;
-      at = next;
+  }
+  if (warp == 2) {
+    // The tile table.  Offsets are device data: kept within [0, M] and in
+    // order (a running maximum), so that no address below depends on their
+    // being right.  A lane takes eight experts.
+    int o[9];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) {
+      const int e = lane * 8 + i;
+      o[i] = p.offsets && e <= E ? min(max(__ldg(p.offsets + e), 0), p.M) : (e == 0 ? 0 : p.M);
+      if (i > 0) o[i] = max(o[i], o[i - 1]);
     }
-    st->off[E] = at;
-    st->tile_start[E] = acc;
-    st->total_tiles = acc;
+    int high = o[8];                             // over the lanes before
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, high, d);
+      if (lane >= d) high = max(high, v);
+    }
+    high = __shfl_up_sync(0xffffffffu, high, 1);
+    if (lane == 0) high = 0;
+    int tiles[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 9; ++i) o[i] = max(o[i], high);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      tiles[i] = lane * 8 + i < E ? (o[i + 1] - o[i] + C::TILE_M - 1) / C::TILE_M * n_tiles : 0;
+      sum += tiles[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    int at = incl - sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      if (e <= E) {
+        st->off[e] = o[i];
+        st->tile_start[e] = at;
+      }
+      at += tiles[i];
+    }
+    if (lane == 31) {
+      st->total_tiles = at;
+      if (E == kMaxExperts) {
+        st->off[E] = o[8];
+        st->tile_start[E] = at;
+      }
+    }
   }
   if (warp == 0 && lane == 0) tma_prefetch_desc(&tmB);
   if (warp == 1) tmem_get<PAIR>(&st->tmem_base);
@@ -636,6 +714,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t par = 0;
     uint32_t g = 0;                              // groups of scales taken so far
     int n = 0;                                   // tiles begun before this one
+    // kFew: the rows of tile tl that are this warp's, from the sums in part
+    auto few_rows = [&](const Tile& tl, int n) {
+      warp_wait(&st->xfull[0], n & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
+      const int rows = min(C::TILE_M, tl.rows);
+      for (int r = warp - EPI_WARP0; r < rows; r += EPI_WARPS) {
+        const float4* src = reinterpret_cast<const float4*>(st->part[r]) + lane;
+        finish_row<EPI>(p, tl, r, lane, src[0], src[32]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&st->xempty);
+    };
+    if (quad >= C::QUADS && split == 1)
+      for (int t = worker, m = 0; t < total; t += workers, ++m) few_rows(tile_of(t), m);
     for (int t = quad < C::QUADS ? worker : total; t < total; t += workers, ++n) {
       const Tile tl = tile_of(t);
       const int rows = min(tl.rows - static_cast<int>(rank) * BM, MODE == kFew ? C::TILE_M : BM);
@@ -653,6 +744,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t sbuf = g & 1u;
         warp_wait(&st->sfull[sbuf], (g >> 1) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
         const float* sa = &st->sa[sbuf][0][r];
+        constexpr int kRows = 32 * C::QUADS;
         const float2* sw = st->sw[sbuf];
         const int nk = min(SCALE_KB, kb_hi - k0);
         float a = sa[0];
@@ -669,7 +761,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const f32x2 s0 = both(a * w.x), s1 = both(a * w.y);
           const int kn = min(k + 1, SCALE_KB - 1);
-          a = sa[kn * BM];
+          a = sa[kn * kRows];
           w = sw[kn];
           if (live) {
             tmem_ld_wait();
@@ -699,24 +791,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         arrive_if<false>(lane == 0, smem_u32(&st->sempty[sbuf]));
       }
 
-      if (split > 1) {
-        // this CTA's share of the sums into the ring, once both halves' MMAs
-        // have read their last block there
-        const int last = kb_hi - kb_lo - 1;
-        warp_wait(&st->empty[last % STAGES], (last / STAGES) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
-        if (rvalid) {
-          float* dst = reinterpret_cast<float*>(smem) + r * kPartStride + half * 64;
+      if constexpr (MODE == kFew) {
+        // The sums go through shared memory, from where all epilogue warps
+        // finish them, a warp per row: on this warp alone, 64 lots of silu and
+        // a row of stores took 4 us a tile.
+        if (n > 0) warp_wait(&st->xempty, (n - 1) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
+        float* dst = &st->part[r][half * 64];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 x = unpack(acc[c][2 * j]), y = unpack(acc[c][2 * j + 1]);
-              *reinterpret_cast<float4*>(dst + c * 128 + 4 * j) = make_float4(x.x, x.y, y.x, y.y);
-            }
-        }
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = unpack(acc[c][2 * j]), y = unpack(acc[c][2 * j + 1]);
+            *reinterpret_cast<float4*>(dst + c * 128 + 4 * j) = make_float4(x.x, x.y, y.x, y.y);
+          }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st->xfull[0]);
+        if (split == 1) few_rows(tl, n);
         continue;
       }
-      if constexpr (EPI == kSiluQuant) {
+      if constexpr (MODE != kFew && EPI == kSiluQuant) {
         // columns [half * 64, half * 64 + 64) of the tile's 128
         const int parity = n & 1;
         const int col0 = tl.n_blk * 128 + half * 64;
@@ -800,44 +893,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int rows = min(C::TILE_M, tl.rows);
         for (int r = share + (warp - EPI_WARP0) * split; r < rows; r += EPI_WARPS * split) {
           float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-          const uint32_t at = smem_u32(smem) + (r * kPartStride + 4 * lane) * 4;
+          const uint32_t at = smem_u32(&st->part[r][4 * lane]);
           for (int q = 0; q < split; ++q) {
             const float4 x = ld_cluster(at, q), y = ld_cluster(at + 512, q);
             s0.x += x.x; s0.y += x.y; s0.z += x.z; s0.w += x.w;
             s1.x += y.x; s1.y += y.y; s1.z += y.z; s1.w += y.w;
           }
-          const size_t grow = static_cast<size_t>(tl.row0 + r) * p.n_out;
-          if constexpr (EPI == kSiluQuant) {
-            const int col = tl.n_blk * 128 + 4 * lane;
-            const bool in = col < p.n_out;       // n_out is a multiple of 16
-            float4 h;
-            h.x = in ? silu_bf16_epilogue(s0.x) * s1.x : 0.f;
-            h.y = in ? silu_bf16_epilogue(s0.y) * s1.y : 0.f;
-            h.z = in ? silu_bf16_epilogue(s0.z) * s1.z : 0.f;
-            h.w = in ? silu_bf16_epilogue(s0.w) * s1.w : 0.f;
-            const float s = fp8_scale(warp_max(fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)))));
-            const float inv = 1.f / s;
-            if (in)
-              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + grow + col) =
-                  fp8_pack4(h.x * inv, h.y * inv, h.z * inv, h.w * inv);
-            if (lane == 0)
-              p.out_scales[static_cast<size_t>(tl.row0 + r) * ((p.n_out + 127) / 128) + tl.n_blk] = s;
-          } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int col = tl.n_blk * 256 + c * 128 + 4 * lane;
-              const float4 v = c ? s1 : s0;
-              if (col >= p.n_out) continue;      // n_out is a multiple of 8
-              if constexpr (EPI == kOutBf16) {
-                uint2 w;
-                reinterpret_cast<__nv_bfloat162*>(&w)[0] = __floats2bfloat162_rn(v.x, v.y);
-                reinterpret_cast<__nv_bfloat162*>(&w)[1] = __floats2bfloat162_rn(v.z, v.w);
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + grow + col) = w;
-              } else {
-                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + grow + col) = v;
-              }
-            }
-          }
+          finish_row<EPI>(p, tl, r, lane, s0, s1);
         }
       }
       cluster_sync_all();                      // no CTA leaves while its share may be read
@@ -887,53 +949,51 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workers (CTAs or pairs) that the device runs at once; sets the kernel's
-// shared-memory opt-in on the way.  Asked once per device and kernel.
+// Clusters of `size` CTAs (1: single CTAs) that the device runs at once; sets
+// the kernel's shared-memory opt-in on the way.  A cluster stays within a GPC,
+// so of 8 CTAs some 15 fit on 148 SMs.  Asked once per device, kernel and size.
 template <int EPI, int MODE>
-cudaError_t resident_workers(int* out) {
-  constexpr bool PAIR = MODE == kPair;
+cudaError_t resident_clusters(int size, int* out) {
   static std::mutex mu;
-  static int known[64] = {};
+  static int known[64][9] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
-  if (dev >= 0 && dev < 64 && known[dev] > 0) {
-    *out = known[dev];
-    return cudaSuccess;
+  if (known[dev][size] == 0) {
+    constexpr int bytes = static_cast<int>(smem_bytes<MODE>());
+    err = cudaFuncSetAttribute(gemm_fp8_kernel<EPI, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != cudaSuccess) return err;
+    int n = num_sms() / size;
+    if (size > 1) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(n * size);
+      cfg.blockDim = dim3(THREADS);
+      cfg.dynamicSmemBytes = bytes;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = size;
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int fit = 0;
+      if (cudaOccupancyMaxActiveClusters(&fit, gemm_fp8_kernel<EPI, MODE>, &cfg) == cudaSuccess && fit > 0)
+        n = fit < n ? fit : n;
+      else
+        cudaGetLastError();            // the query is advisory
+    }
+    known[dev][size] = n;
   }
-  constexpr int bytes = static_cast<int>(smem_bytes<MODE>());
-  err = cudaFuncSetAttribute(gemm_fp8_kernel<EPI, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (err != cudaSuccess) return err;
-  int n = PAIR ? num_sms() / 2 : num_sms();
-  if constexpr (PAIR) {
-    // fewer pairs may fit than half the SMs (a pair shares a GPC)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms() / 2 * 2);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = bytes;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int fit = 0;
-    if (cudaOccupancyMaxActiveClusters(&fit, gemm_fp8_kernel<EPI, MODE>, &cfg) == cudaSuccess && fit > 0)
-      n = fit < n ? fit : n;
-    else
-      cudaGetLastError();              // the query is advisory
-  }
-  if (dev >= 0 && dev < 64) known[dev] = n;
-  *out = n;
+  *out = known[dev][size];
   return cudaSuccess;
 }
 
 template <int EPI, int MODE>
 cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, Params p, cudaStream_t s) {
   int workers = 0;
-  const cudaError_t err = resident_workers<EPI, MODE>(&workers);
+  cudaError_t err = resident_clusters<EPI, MODE>(MODE == kPair ? 2 : 1, &workers);
   if (err != cudaSuccess) return err;
   const int bn_out = EPI == kSiluQuant ? 128 : 256;
   const long long n_tiles = (p.n_out + bn_out - 1) / bn_out;
@@ -946,11 +1006,16 @@ cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, Params p, cudaStrea
     return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(2 * pairs), dim3(THREADS), smem_bytes<MODE>(), s, false,
                     2, a, b, p);
   }
-  // At most half as many tiles as SMs: a cluster shares each one's blocks, as
-  // long as every CTA keeps four.
+  // At most half as many tiles as SMs: a cluster shares each one's blocks, of
+  // the largest size of which all run at once and every CTA keeps four.
   p.split = 1;
-  if (MODE == kFew)
-    while (p.split < 8 && bound * p.split * 2 <= workers && p.num_kb >= 8 * p.split) p.split *= 2;
+  if (MODE == kFew && bound * 2 <= workers)
+    for (int size = 8; size > 1 && p.split == 1; --size) {
+      int fit = 0;
+      if (bound * size > workers || p.num_kb < 4 * size) continue;
+      if ((err = resident_clusters<EPI, MODE>(size, &fit)) != cudaSuccess) return err;
+      if (bound <= fit) p.split = size;
+    }
   if (p.split > 1)
     return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(static_cast<unsigned>(bound * p.split)), dim3(THREADS),
                     smem_bytes<MODE>(), s, false, p.split, a, b, p);
