@@ -133,6 +133,7 @@ struct Tail {
   // kFew: the tile's sums, a row of 256 columns after the other; 16 bytes more
   // per row keep row-per-lane accesses free of bank conflicts
   alignas(16) float part[MODE == kFew ? 32 : 1][kPartStride];
+  alignas(16) uint8_t stage[MODE == kFew ? 1 : EPI_WARPS][2048];   // an epilogue warp's way out
   alignas(16) float2 sw[2][SCALE_KB];   // of the first and the second 128 weight rows
 };
 
@@ -298,6 +299,11 @@ __device__ __forceinline__ void fma2(f32x2& acc, uint32_t x, uint32_t y, f32x2 s
                : "+l"(acc)
                : "r"(x), "r"(y), "l"(s));
 }
+__device__ __forceinline__ f32x2 pack(float2 v) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
 __device__ __forceinline__ float2 unpack(f32x2 v) {
   float2 r;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
@@ -361,6 +367,28 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok));
   return ok != 0;
+}
+
+// 64 bytes of each of 32 rows, a row per lane in w, to rows `row_bytes` apart
+// from `out` on, at byte `at` of each: through 2 KB of shared memory, so that
+// four lanes store a row's 64 bytes (16 bytes to 32 rows at once, straight from
+// the lanes, took 1.6 us a tile).  Stores rows below `rows`, bytes below
+// row_bytes.  16-byte unit u of row r lies at u ^ (r / 2 % 4): no bank
+// conflicts in either direction.
+__device__ __forceinline__ void store_rows(uint8_t* stg, int lane, const uint4 (&w)[4], uint8_t* out,
+                                           size_t row_bytes, size_t at, int rows) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    *reinterpret_cast<uint4*>(stg + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = w[u];
+  __syncwarp();
+  const int u = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+    if (r < rows && at + 16 * u < row_bytes) *reinterpret_cast<uint4*>(out + r * row_bytes + at + 16 * u) = v;
+  }
+  __syncwarp();
 }
 
 // One row of a tile from its sums, by a warp: a lane has columns 4 * lane .. + 3
@@ -809,74 +837,86 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (split == 1) few_rows(tl, n);
         continue;
       }
+      uint8_t* stg = st->stage[warp - EPI_WARP0];
+      const int row_in = quad * 32 + static_cast<int>(rank) * BM;      // this warp's first row in the tile
+      const int nrows = tl.rows - row_in;                              // (may be none, or more than 32)
       if constexpr (MODE != kFew && EPI == kSiluQuant) {
         // columns [half * 64, half * 64 + 64) of the tile's 128
         const int parity = n & 1;
         const int col0 = tl.n_blk * 128 + half * 64;
         float m = 0.f;
-        float h[64];
+        if (live) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float2 gt = unpack(acc[0][j]), up = unpack(acc[1][j]);
-          const bool in = col0 + 2 * j < p.n_out;
-          h[2 * j] = in ? silu_bf16_epilogue(gt.x) * up.x : 0.f;
-          h[2 * j + 1] = in ? silu_bf16_epilogue(gt.y) * up.y : 0.f;
-          m = fmaxf(m, fmaxf(fabsf(h[2 * j]), fabsf(h[2 * j + 1])));
+          for (int c = 0; c < 4; ++c) {          // n_out is a multiple of 16
+            if (col0 + 16 * c < p.n_out) {
+#pragma unroll
+              for (int j = 8 * c; j < 8 * c + 8; ++j) {
+                const float2 gt = unpack(acc[0][j]), up = unpack(acc[1][j]);
+                const float2 h = make_float2(silu_bf16_epilogue(gt.x) * up.x, silu_bf16_epilogue(gt.y) * up.y);
+                acc[0][j] = pack(h);
+                m = fmaxf(m, fmaxf(fabsf(h.x), fabsf(h.y)));
+              }
+            } else {
+#pragma unroll
+              for (int j = 8 * c; j < 8 * c + 8; ++j) acc[0][j] = 0ull;
+            }
+          }
         }
         st->amax[parity][half][r] = m;
         // meet the other half's warps
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->xfull[parity]);
         warp_wait(&st->xfull[parity], (n >> 1) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
-        m = fmaxf(st->amax[parity][0][r], st->amax[parity][1][r]);
-        const float s = fp8_scale(m);
-        const float inv = 1.f / s;
-        if (rvalid) {
-          uint8_t* q = static_cast<uint8_t*>(p.out) + static_cast<size_t>(grow) * p.n_out + col0;
+        if (live) {
+          m = fmaxf(st->amax[parity][0][r], st->amax[parity][1][r]);
+          const float s = fp8_scale(m);
+          const float inv = 1.f / s;
+          uint4 w[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (col0 + 16 * c < p.n_out) {       // n_out is a multiple of 16
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float* f = h + 16 * c + 4 * j;
-                w[j] = fp8_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-              }
-              *reinterpret_cast<uint4*>(q + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          if (half == 0)
-            p.out_scales[static_cast<size_t>(grow) * ((p.n_out + 127) / 128) + tl.n_blk] = s;
-        }
-        __syncwarp();
-      } else if (rvalid) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col0 = tl.n_blk * 256 + c * 128 + half * 64;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {          // 8 columns: n_out is a multiple of 8
-            const int col = col0 + 8 * j;
-            if (col >= p.n_out) continue;
-            float a[8];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float2 f = unpack(acc[c][4 * j + q]);
-              a[2 * q] = f.x;
-              a[2 * q + 1] = f.y;
+              const float2 f = unpack(acc[0][8 * c + 2 * q]), g2 = unpack(acc[0][8 * c + 2 * q + 1]);
+              x[q] = fp8_pack4(f.x * inv, f.y * inv, g2.x * inv, g2.y * inv);
             }
-            const size_t o = static_cast<size_t>(grow) * p.n_out + col;
-            if constexpr (EPI == kOutBf16) {
-              uint4 w;
-              __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&w);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) b[q] = __floats2bfloat162_rn(a[2 * q], a[2 * q + 1]);
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o) = w;
-            } else {
-              float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
-              d[0] = make_float4(a[0], a[1], a[2], a[3]);
-              d[1] = make_float4(a[4], a[5], a[6], a[7]);
-            }
+            w[c] = make_uint4(x[0], x[1], x[2], x[3]);
           }
+          store_rows(stg, lane, w, static_cast<uint8_t*>(p.out) + static_cast<size_t>(tl.row0 + row_in) * p.n_out,
+                     p.n_out, col0, nrows);
+          if (half == 0 && rvalid)
+            p.out_scales[static_cast<size_t>(grow) * ((p.n_out + 127) / 128) + tl.n_blk] = s;
         }
+      } else if (MODE != kFew && live) {
+        constexpr int kBytes = EPI == kOutBf16 ? 2 : 4;
+        uint8_t* out = static_cast<uint8_t*>(p.out) + static_cast<size_t>(tl.row0 + row_in) * p.n_out * kBytes;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k = 0; k < kBytes; ++k) {     // 64 bytes of a row at a time
+            const int col = tl.n_blk * 256 + c * 128 + half * 64 + k * (64 / kBytes);
+            if (col >= p.n_out) continue;        // n_out is a multiple of 8: whole 16 bytes
+            uint4 w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const f32x2* a = acc[c] + k * (32 / kBytes) + u * (8 / kBytes);
+              uint32_t x[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if constexpr (EPI == kOutBf16) {
+                  const float2 f = unpack(a[q]);
+                  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+                  x[q] = *reinterpret_cast<const uint32_t*>(&b);
+                } else {
+                  const float2 f = unpack(a[q / 2]);
+                  x[q] = __float_as_uint(q & 1 ? f.y : f.x);
+                }
+              }
+              w[u] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            store_rows(stg, lane, w, out, static_cast<size_t>(p.n_out) * kBytes,
+                       static_cast<size_t>(col) * kBytes, nrows);
+          }
       }
       __syncwarp();
     }
