@@ -69,8 +69,6 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr int kBoxes = 5;                      // A boxes of 8, 16, 32, 64 and 128 rows
 constexpr int kRowGroup = 16;                  // row blocks that share a pass over the weights
 
-constexpr long long kPairRows = 192;           // rows per expert from which pairs run
-constexpr long long kFewRows = 32;             // and up to which the 32-row form does
 
 // kOne: a CTA, 128 rows.  kPair: a CTA pair, 256 rows.  kFew: a CTA, 32 rows.
 enum { kOne = 0, kPair = 1, kFew = 2 };
@@ -1100,8 +1098,17 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   p.out = g.out;
   p.out_scales = g.q_scales;
   p.err = g.err;
-  // by the rows of an expert, on average
-  const int mode = g.M <= kFewRows * g.E ? kFew : !g.gather && g.M >= kPairRows * g.E ? kPair : kOne;
+  // By the rows of an expert on average.  Us a product, 32 rows | one CTA | pair:
+  // 16 experts of 2048 x 2048, 24 rows each: 19 | 19 | 27, 32 rows: 27 | 20 | 27,
+  // 512 rows: 138 | 57 | 58; 64 experts of 2816 x 2048, 512 rows each: one CTA
+  // 244, pair 257 (half a pair tile of padding per expert); 8192 rows of 4096 x
+  // 14336: one CTA 470, pair 435.  Where one CTA per tile would leave half the
+  // SMs idle, the 32-row form shares tiles out: 64 rows of 4096 x 4096: 17 | 21,
+  // 128 rows: 21 | 21.
+  const long long few_tiles = ((g.M + BM - 1) / BM + (g.E > 1 ? g.E : 0)) * ((g.N + 255) / 256);
+  int mode = g.M <= 24LL * g.E || (g.M <= 96LL * g.E && few_tiles * 2 <= num_sms()) ? kFew : kOne;
+  if (g.M >= 768LL * g.E) mode = kPair;
+  if (g.gather) mode = kFew;                     // the only form that fetches rows by token
   AMaps ma;
   CUtensorMap mb;
   for (int i = 0; i < kBoxes; ++i)
