@@ -389,8 +389,8 @@ MOE_API moe_status_t moe_gemm_fp8(const void* a, const float* a_scales, const vo
  * A slot whose index lies outside [0, E) is unused: it adds nothing, and its
  * weight is not read as a number (padded tokens get a row of zeros).  The
  * same expert twice in a token counts twice.  The intermediate is rounded to
- * 8 bits once, each expert's output to bf16 once, the weighted sum (fp32, in
- * slot order) to bf16 once.  D and F must be multiples of 16.  With the stage
+ * 8 bits once, each expert's output to block-scaled fp16 once, the weighted
+ * sum (fp32, in slot order) to bf16 once.  D and F must be multiples of 16.  With the stage
  * profiler on the call is recorded like a forward (no router stage).
  */
 MOE_API size_t moe_experts_workspace_size_fp8(int64_t T, int64_t D, int64_t F, int E, int K);

@@ -21,6 +21,21 @@ constexpr float kQuantFloor = 7.888609052210118e-31f;   // 2^-100
 // The scale of a block from its largest magnitude.
 __device__ __forceinline__ float fp8_scale(float amax) { return fmaxf(amax, kQuantFloor) / kFp8Max; }
 
+// v / scale for the values v of one block, from multiples u of them: u * 448 /
+// max|u| is the same quotient with fewer roundings.  For bf16 values, and for
+// products of two, u * 448 is exact in fp32, so that a quotient which is a tie
+// of the rounding to e4m3 is one here too: the product with the reciprocal is
+// corrected by its exact remainder (Markstein's final step, 1990), two FMAs;
+// IEEE divisions made the norm of 16384 x 2048 values 52 -> 59 us.
+__device__ __forceinline__ bool fp8_direct(float largest_u) {   // far from fp32's ends
+  return largest_u > 1e-30f && largest_u < 1e30f;
+}
+__device__ __forceinline__ float fp8_quotient(float u, float largest_u, float reciprocal) {
+  const float a = u * kFp8Max;
+  const float q = a * reciprocal;
+  return fmaf(fmaf(-q, largest_u, a), reciprocal, q);
+}
+
 // Two values to packed e4m3 (the first in the low byte), nearest even,
 // saturating at +-448.
 __device__ __forceinline__ uint16_t fp8_pack2(float lo, float hi) {

@@ -186,7 +186,7 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Workspace of moe_experts_forward_fp8.
 struct Layout {
-  size_t idx32, bcount, bbase, totals, offsets, perm, pos, xperm, h, hscales, y, total;
+  size_t idx32, bcount, bbase, totals, offsets, perm, pos, xperm, h, hscales, y, yscales, total;
   int B;
   bool gather;      // gate_up fetches its rows of x by token
 };
@@ -214,6 +214,7 @@ Layout layout(int64_t T, int64_t D, int64_t F, int E, int K) {
   L.h = take(static_cast<size_t>(R) * F);
   L.hscales = take(sizeof(float) * R * ((F + kQuantBlock - 1) / kQuantBlock));
   L.y = take(2 * static_cast<size_t>(R) * D);
+  L.yscales = take(sizeof(float) * R * ((D + 63) / 64));
   L.total = o;
   return L;
 }
@@ -513,13 +514,15 @@ moe_status_t moe_experts_forward_fp8(const void* x_fp8, const float* x_scales,
   d.N = Di;
   d.K = Fi;
   d.out = ws + L.y;
+  d.f16_scales = reinterpret_cast<float*>(ws + L.yscales);
   d.err = err;
   scope.begin();
   if ((st = launched(launch_gemm_fp8(d, s), s, "down fp8 GEMM")) != MOE_OK) return st;
   scope.end(3);
 
   scope.begin();
-  st = launched(launch_combine(ws + L.y, routing_weights, pos, Ti, K, Di, kBF16, out, s), s, "combine");
+  st = launched(launch_combine_f16(ws + L.y, d.f16_scales, routing_weights, pos, Ti, K, Di, out, s), s,
+                "combine");
   if (st != MOE_OK) return st;
   scope.end(4);
   return MOE_OK;

@@ -41,6 +41,10 @@
 //
 // Epilogues (columns of the output per tile):
 //   kOutBf16, kOutF32   the sums, rounded once (256 columns);
+//   kOutF16             the sums in fp16 times a power of two, one for each 64
+//                       columns of a row: what the experts' outputs are kept
+//                       in until they are summed.  bf16 would take the same
+//                       bytes and round eight times as coarsely;
 //   kSiluQuant          h = silu(gate) * up in fp32, then e4m3 with one scale
 //                       for the row's 128 columns: a row's largest |h| is a
 //                       maximum over the two threads (halves) that share it.
@@ -48,6 +52,8 @@
 // Rows outside [offsets[0], offsets[E]) are not touched.  Every mbarrier wait
 // is bounded (common.cuh); after a timeout the epilogue runs through its loop
 // without waiting, so that no warp is left at a barrier.
+#include <cuda_fp16.h>
+
 #include <mutex>
 
 #include "common.cuh"
@@ -83,7 +89,7 @@ struct Cfg {
   static constexpr int QUADS = MODE == kFew ? 1 : 4;   // groups of 32 TMEM lanes with rows
 };
 
-enum { kOutBf16 = 0, kOutF32 = 1, kSiluQuant = 2 };
+enum { kOutBf16 = 0, kOutF32 = 1, kSiluQuant = 2, kOutF16 = 3 };
 
 struct AMaps {
   CUtensorMap m[kBoxes];
@@ -104,7 +110,7 @@ struct Params {
   const float* sa;       // (rows, num_kb)
   const float* sw;       // (E, w_blocks, num_kb)
   void* out;             // (M, n_out) bf16, fp32 or e4m3
-  float* out_scales;     // (M, ceil(n_out / 128)), kSiluQuant
+  float* out_scales;     // (M, ceil(n_out / 128)), kSiluQuant; (M, ceil(n_out / 64)), kOutF16
   unsigned int* err;
 };
 
@@ -367,6 +373,19 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// The power of two that brings a block with largest magnitude amax to the top
+// of fp16's range (its inverse is what is stored); 1 for zeros, infinities
+// and NaN.
+__device__ __forceinline__ float f16_scale(float amax) {
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23);         // biased exponent, amax >= 0
+  if (e == 0 || e == 255) return 1.f;
+  return __uint_as_float(static_cast<uint32_t>(min(max(127 + 14 - (e - 127), 1), 254)) << 23);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // 64 bytes of each of 32 rows, a row per lane in w, to rows `row_bytes` apart
 // from `out` on, at byte `at` of each: through 2 KB of shared memory, so that
 // four lanes store a row's 64 bytes (16 bytes to 32 rows at once, straight from
@@ -414,6 +433,19 @@ __device__ __forceinline__ void finish_row(const Params& p, const Tile& tl, int 
     for (int c = 0; c < 2; ++c) {
       const int col = tl.n_blk * 256 + c * 128 + 4 * lane;
       const float4 v = c ? v1 : v0;
+      if constexpr (EPI == kOutF16) {
+        const bool in = col < p.n_out;           // columns past it: another expert's, not to be looked at
+        float m = in ? fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))) : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = f16_scale(m);
+        if (in)
+          *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + grow + col) =
+              make_uint2(pack_f16x2(v.x * s, v.y * s), pack_f16x2(v.z * s, v.w * s));
+        if (in && (lane & 15) == 0)
+          p.out_scales[static_cast<size_t>(tl.row0 + r) * ((p.n_out + 63) / 64) + col / 64] = 1.f / s;
+        continue;
+      }
       if (col >= p.n_out) continue;              // n_out is a multiple of 8
       if constexpr (EPI == kOutBf16) {
         uint2 w;
@@ -886,10 +918,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             p.out_scales[static_cast<size_t>(grow) * ((p.n_out + 127) / 128) + tl.n_blk] = s;
         }
       } else if (MODE != kFew && live) {
-        constexpr int kBytes = EPI == kOutBf16 ? 2 : 4;
+        constexpr int kBytes = EPI == kOutF32 ? 4 : 2;
         uint8_t* out = static_cast<uint8_t*>(p.out) + static_cast<size_t>(tl.row0 + row_in) * p.n_out * kBytes;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          float s = 1.f;
+          if constexpr (EPI == kOutF16) {        // 64 columns in this thread: a block
+            const int col = tl.n_blk * 256 + c * 128 + half * 64;
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float2 f = unpack(acc[c][j]);
+              if (col + 2 * j < p.n_out) m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            s = f16_scale(m);
+            if (rvalid && col < p.n_out)
+              p.out_scales[static_cast<size_t>(grow) * ((p.n_out + 63) / 64) + col / 64] = 1.f / s;
+          }
 #pragma unroll
           for (int k = 0; k < kBytes; ++k) {     // 64 bytes of a row at a time
             const int col = tl.n_blk * 256 + c * 128 + half * 64 + k * (64 / kBytes);
@@ -901,7 +946,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               uint32_t x[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                if constexpr (EPI == kOutBf16) {
+                if constexpr (EPI == kOutF16) {
+                  const float2 f = unpack(a[q]);
+                  x[q] = pack_f16x2(f.x * s, f.y * s);
+                } else if constexpr (EPI == kOutBf16) {
                   const float2 f = unpack(a[q]);
                   const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
                   x[q] = *reinterpret_cast<const uint32_t*>(&b);
@@ -915,6 +963,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             store_rows(stg, lane, w, out, static_cast<size_t>(p.n_out) * kBytes,
                        static_cast<size_t>(col) * kBytes, nrows);
           }
+        }
       }
       __syncwarp();
     }
@@ -1071,6 +1120,7 @@ template <int MODE>
 cudaError_t launch_mode(const GemmFp8Args& g, const AMaps& a, const CUtensorMap& b, const Params& p,
                         cudaStream_t s) {
   if (g.q_scales) return launch_epi<kSiluQuant, MODE>(a, b, p, s);
+  if (g.f16_scales) return launch_epi<kOutF16, MODE>(a, b, p, s);
   if (g.out_f32) return launch_epi<kOutF32, MODE>(a, b, p, s);
   return launch_epi<kOutBf16, MODE>(a, b, p, s);
 }
@@ -1096,7 +1146,7 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   p.sa = g.a_scales;
   p.sw = g.w_scales;
   p.out = g.out;
-  p.out_scales = g.q_scales;
+  p.out_scales = gated ? g.q_scales : g.f16_scales;
   p.err = g.err;
   // By the rows of an expert on average.  Us a product, 32 rows | one CTA | pair:
   // 16 experts of 2048 x 2048, 24 rows each: 19 | 19 | 27, 32 rows: 27 | 20 | 27,

@@ -199,9 +199,15 @@ struct GemmFp8Args {
   void* out;
   bool out_f32;
   float* q_scales;
+  float* f16_scales;       // set: out is fp16 times these, one per row and 64 columns
   unsigned int* err;
 };
 cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s);
+
+// out[t, :] = sum_k w[t, k] * Y[pos[t, k], :] in bf16, Y in fp16 with a scale
+// per row and 64 columns; fp32 sum in k order; slots with pos < 0 add nothing.
+cudaError_t launch_combine_f16(const void* Y, const float* scales, const float* w, const int* pos, int T,
+                               int K, int D, void* out, cudaStream_t s);
 
 // 32-token histograms and 32-bit copy of a given selection; an index outside
 // [0, E) becomes E (an unused slot).

@@ -105,33 +105,51 @@ struct Unit {
       }
     }
   }
-  // The unit's blocks to e4m3 and their scales (one per 16 lanes, or one).
-  __device__ static void quantize(uint8_t* qrow, float* srow, int u, int lane, int D,
-                                  const float (&v)[N]) {
+  // The largest |v| of this lane's block (16 lanes, or the warp).
+  __device__ static float largest(const float (&v)[N]) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
 #pragma unroll
     for (int o = kVec ? 8 : 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float s = fp8_scale(m);
-    const float inv = 1.f / s;
+    return m;
+  }
+  // The unit's blocks of v = u * by to e4m3 and their scales.
+  __device__ static void quantize(uint8_t* qrow, float* srow, int unit, int lane, int D,
+                                  const float (&v)[N], const float (&u)[N], float by) {
+    const float m = largest(u);
+    float amax = m * by;
+    const bool direct = fp8_direct(m) && amax >= kQuantFloor;
+    float t[N];
+    if (__any_sync(0xffffffffu, !direct)) {      // zeros, extremes: from v itself
+      const float mv = largest(v);               // (all lanes meet in it)
+      amax = direct ? amax : mv;
+      const float s = fp8_scale(amax);
+#pragma unroll
+      for (int i = 0; i < N; ++i) t[i] = v[i] / s;
+    } else {
+      const float r = 1.f / m;
+#pragma unroll
+      for (int i = 0; i < N; ++i) t[i] = fp8_quotient(u[i], m, r);
+    }
+    const float s = fp8_scale(amax);
     if constexpr (kVec) {
-      const int c = u * 256 + lane * 8;
+      const int c = unit * 256 + lane * 8;
       if (c < D) {
         uint2 q;
-        q.x = fp8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-        q.y = fp8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+        q.x = fp8_pack4(t[0], t[1], t[2], t[3]);
+        q.y = fp8_pack4(t[4], t[5], t[6], t[7]);
         *reinterpret_cast<uint2*>(qrow + c) = q;
         if ((lane & 15) == 0) srow[c / kQuantBlock] = s;
       }
     } else {
-      if (u * 128 < D) {
+      if (unit * 128 < D) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int c = col(u, lane, i);
-          if (c < D) qrow[c] = static_cast<uint8_t>(fp8_pack2(v[i] * inv, 0.f));
+          const int c = col(unit, lane, i);
+          if (c < D) qrow[c] = static_cast<uint8_t>(fp8_pack2(t[i], 0.f));
         }
-        if (lane == 0) srow[u] = s;
+        if (lane == 0) srow[unit] = s;
       }
     }
   }
@@ -205,13 +223,16 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
     const int u = warp + j * warps;
     if constexpr (!kEarly) L::load(w, u, lane, D, wv[0]);
     if (a.sum_out) L::store(static_cast<T*>(a.sum_out) + row, u, lane, D, h[j]);
-    float y[L::N];
+    float y[L::N], hw[L::N];                     // hw: exact for bf16, what the blocks are divided from
 #pragma unroll
-    for (int i = 0; i < L::N; ++i) y[i] = h[j][i] * rstd * wv[kEarly ? j : 0][i];
+    for (int i = 0; i < L::N; ++i) {
+      hw[i] = h[j][i] * wv[kEarly ? j : 0][i];
+      y[i] = h[j][i] * rstd * wv[kEarly ? j : 0][i];
+    }
     if (a.out) L::store(static_cast<T*>(a.out) + row, u, lane, D, y);
     if (a.q) {
       const int nb = (D + kQuantBlock - 1) / kQuantBlock;
-      L::quantize(a.q + row, a.scales + static_cast<size_t>(blockIdx.x) * nb, u, lane, D, y);
+      L::quantize(a.q + row, a.scales + static_cast<size_t>(blockIdx.x) * nb, u, lane, D, y, hw, rstd);
     }
   }
 }
@@ -253,7 +274,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* x, int64_t 
   const int u = static_cast<int>(at - row * units);
   float v[L::N];
   L::load(x + row * D, u, lane, D, v);
-  L::quantize(q + row * D, scales + row * nb, u, lane, D, v);
+  L::quantize(q + row * D, scales + row * nb, u, lane, D, v, v, 1.f);
 }
 
 // Matrices: a CTA per 128 x 128 block; a warp takes 16 of its rows, a lane
@@ -285,14 +306,16 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* x, int ro
 #pragma unroll
   for (int w = 0; w < 8; ++w) m = fmaxf(m, part[w]);
   const float s = fp8_scale(m);
-  const float inv = 1.f / s;
+  const bool direct = fp8_direct(m);
+  const float inv = 1.f / m;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = br * kQuantBlock + i * 8 + warp, c = bc * kQuantBlock + j * 32 + lane;
       if (r < rows && c < cols)
-        q[base + static_cast<int64_t>(r) * cols + c] = static_cast<uint8_t>(fp8_pack2(v[i][j] * inv, 0.f));
+        q[base + static_cast<int64_t>(r) * cols + c] = 
+            static_cast<uint8_t>(fp8_pack2(direct ? fp8_quotient(v[i][j], m, inv) : v[i][j] / s, 0.f));
     }
   if (threadIdx.x == 0) scales[b] = s;
 }
