@@ -243,9 +243,13 @@ cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t s) {
   // fit: 64 bytes of each tensor per thread, which keeps more loads in flight
   // per SM and has fewer warps meet at a row's barrier (16384 x 2048 bf16 with
   // a residual: 57 us with 16 bytes, 54 with 32, 52 with 64; 4096 x 5120 fp32:
-  // 62 us with 32, 60 with 64, 68 with 128).
+  // 62 us with 32, 60 with 64, 68 with 128).  Where lanes load single values,
+  // four units at most and four warps a row: the chain of a unit's 4 values is
+  // longer there and wants warps to hide it (9000 x 2567 bf16: 103 us with 8
+  // units of a warp, 86 with 4, 90 with 2, 97 with 1; 12000 x 516: 43, 43, 31, 28).
   const int units = (a.D + Unit<kVec>::kCols - 1) / Unit<kVec>::kCols;
-  int U = rows <= 2 * num_sms() ? 1 : 64 / (Unit<kVec>::N * static_cast<int>(sizeof(T)));
+  int U = rows <= 2 * num_sms() ? 1 : kVec ? 8 / static_cast<int>(sizeof(T)) : 4;
+  while (!kVec && U > 1 && units < 4 * U) U /= 2;
   while (U > 1 && U > units) U /= 2;
   while (units > 32 * U) U *= 2;
   const dim3 grid(static_cast<unsigned>(rows)), block(32 * ((units + U - 1) / U));

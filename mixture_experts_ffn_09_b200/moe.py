@@ -451,9 +451,9 @@ def _want(t, shape, dtype, name, dev, required=True):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev >= 0:
+    if t.get_device() != dev or dev < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
     return t.data_ptr()
 
