@@ -257,6 +257,51 @@ def test_product_by_expert(E, M, N, K, offsets):
     check_product(E, M, N, K, offsets, torch.float32, seed=50)
 
 
+def uneven(M, E, *rows):
+    """Offsets of E experts over M rows: the given row counts first, the rest by turns."""
+    o = [0]
+    for r in rows:
+        o.append(min(M, o[-1] + r))
+    left = E - len(rows)
+    return o + [o[-1] + (M - o[-1]) * (i + 1) // left for i in range(left)]
+
+
+@pytest.mark.parametrize("E,M,N,K,offsets", [
+    (1, 16, 24, 4096, None),                             # few tiles: the K blocks over a cluster
+    (3, 70, 40, 2064, [0, 33, 33, 70]),
+    (64, 1500, 264, 272, uneven(1500, 64, 3, 1400)),     # 32-row tiles, most of them one expert's
+    (8, 800, 2056, 144, uneven(800, 8, 1, 0, 700)),
+    (8, 5000, 304, 144, uneven(5000, 8, 0, 2500, 129)),  # 128-row tiles, more than 16 row blocks of an expert
+    (2, 2000, 520, 400, [3, 903, 1990]),                 # pairs of CTAs with tails; rows around them stay
+    (2, 1600, 264, 272, [0, 1, 1600]),
+    (3, 2400, 128, 128, [0, 0, 2400, 2400]),
+    (1, 4500, 600, 144, None)], ids=lambda v: "list" if isinstance(v, list) else str(v))
+def test_product_row_forms(E, M, N, K, offsets):
+    check_product(E, M, N, K, offsets, seed=3)
+    check_product(E, M, N, K, offsets, torch.float32, seed=60)
+
+
+def test_products_at_once():
+    """Calls on two streams at the same time, each form with itself and with another."""
+    args = []
+    for i, (E, M, N, K) in enumerate([(1, 16, 256, 4096), (1, 16, 256, 4096), (4, 400, 512, 512), (2, 2000, 512, 512)]):
+        a, sa = rows8(M, K, i)
+        w, sw = weight8(E, N, K, i + 10)
+        o = torch.tensor(uneven(M, E), dtype=torch.int32, device="cuda")
+        args.append((a, sa, w, sw, o))
+    outs = [torch.empty(x[0].shape[0], x[2].shape[1], device="cuda") for x in args]
+    want = [torch.empty_like(o) for o in outs]
+    for x, o in zip(args, want):
+        moe.gemm_fp8(*x[:4], o, offsets=x[4])
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in args]
+    for _ in range(20):
+        for x, o, st in zip(args, outs, s):
+            moe.gemm_fp8(*x[:4], o, offsets=x[4], stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
 def test_product_offsets_out_of_order_are_clamped():
     """Offsets beyond M count as M, descending ones as the one before."""
     a, sa = rows8(40, 128, 1)
@@ -305,13 +350,14 @@ def run_experts(args, stream=None):
 def check_experts(args, out):
     want, raw, bound = R.experts(*args)
     K = args[2].shape[1]
-    # half a step of the intermediate's e4m3, the two roundings to bf16 (each expert's and the sum's)
+    # half a step of the intermediate's e4m3, each expert's rounding (to fp16 with a scale for 64 columns: 2^-11 of
+    # the largest at most) and the sum's to bf16
     mag = want.abs() + bound
     each = sum((args[3][:, k:k + 1].double().abs() for k in range(K)))
     cap = raw.abs().amax(1, keepdim=True) + bound.amax(1, keepdim=True)
     tol = bound * 1.01 + mag * 2.0 ** -8 * 1.01 + each.clamp_min(1) * cap * 2.0 ** -7 + 1e-6
     assert ((out.double() - raw).abs() <= tol).all()
-    # against the rounded intermediate: what is left are the bf16 roundings (2^-8 each at most) and the few
+    # against the rounded intermediate: what is left are the two roundings (2^-8 each at most) and the few
     # values that fall on the other side of a border (a share of 1e-4, each 2^-4 off: 6e-4 in the norm)
     d = (out.double() - want).norm() / want.norm().clamp_min(1e-30)
     assert d <= 2.0 ** -8 + 2.0 ** -8 + 1e-3, float(d)
@@ -325,6 +371,34 @@ def test_experts(T, D, F, E, K):
     out = run_experts(args)
     check_experts(args, out)
     assert torch.equal(out, run_experts(args))
+
+
+@pytest.mark.parametrize("T,D,F,E,K", [(1, 2048, 1152, 2, 1), (3, 2064, 1040, 4, 2),     # K blocks over a cluster
+                                       (600, 256, 400, 8, 2), (2100, 128, 144, 8, 2),      # 128-row tiles
+                                       (1700, 256, 272, 4, 2), (4700, 144, 144, 2, 1)])    # pairs of CTAs
+def test_experts_row_forms(T, D, F, E, K):
+    args = make_experts(T, D, F, E, K, seed=40)
+    out = run_experts(args)
+    check_experts(args, out)
+    args[2][:, 0] = E - 1                        # nearly all to one expert, some slots twice
+    args[2][::7] = -1
+    check_experts(args, run_experts(args))
+    assert (run_experts(args)[::7] == 0).all()
+
+
+def test_experts_at_once():
+    """Two calls on two streams at the same time, a workspace each."""
+    args = [make_experts(24, 512, 384, 8, 2, seed=1), make_experts(300, 256, 384, 8, 2, seed=2)]
+    want = [run_experts(a) for a in args]
+    ws = [torch.empty(moe.experts_workspace_size_fp8(*a[0].shape, 384, 8, 2), dtype=torch.uint8, device="cuda") for a in args]
+    out = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in args]
+    for _ in range(20):
+        for a, o, w, st in zip(args, out, ws, s):
+            moe.experts_forward_fp8(*a, o, workspace=w, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(out, want))
 
 
 @pytest.mark.parametrize("T", [7, 400])
