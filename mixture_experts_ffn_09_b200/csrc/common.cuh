@@ -35,10 +35,6 @@ enum : unsigned int {
   SITE_PAIR_MMA = 1u << 15,
   SITE_PAIR_EPILOGUE = 1u << 16,
   SITE_PROBE = 1u << 17,
-  SITE_FP8_PRODUCER = 1u << 18,
-  SITE_FP8_MMA = 1u << 19,
-  SITE_FP8_EPILOGUE = 1u << 20,
-  SITE_FP8_SCALES = 1u << 21,
 };
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
@@ -129,19 +125,16 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
-}
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
-  return mbar_try(smem_u32(bar), parity);
 }
 
 // Waits for the phase of `bar` with the given parity to complete.  Gives up
@@ -166,70 +159,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       }
     }
   }
-}
-
-// Up to 4096 tries (0.1 ms and more) in a loop of four instructions, for waits
-// on a short loop's critical path: mbar_wait reads %globaltimer as soon as its
-// first try fails, and a try without success so far is the usual case there.
-// False is not final: go on with mbar_wait, out of the usual path.
-__device__ __forceinline__ bool mbar_try_loop(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 0;\n\t"
-      "TRY_%=:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE_%=;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 4096;\n\t"
-      "@q bra TRY_%=;\n\t"
-      "DONE_%=:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// The same for a whole (converged) warp: lane 0 tries, a vote makes the result
-// uniform.
-__device__ __forceinline__ bool mbar_try_loop_warp(uint32_t bar, uint32_t parity, int lane) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred e, p, q;\n\t.reg .u32 n;\n\t"
-      "setp.eq.u32 e, %3, 0;\n\t"
-      "setp.ne.u32 p, 0, 0;\n\t"
-      "mov.u32 n, 0;\n\t"
-      "TRY_%=:\n\t"
-      "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "vote.sync.any.pred p, p, 0xffffffff;\n\t"
-      "@p bra.uni DONE_%=;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 4096;\n\t"
-      "@q bra.uni TRY_%=;\n\t"
-      "DONE_%=:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(static_cast<uint32_t>(lane))
-      : "memory");
-  return ok != 0;
-}
-
-// Tries two barriers at once: their latencies overlap, and one branch on the
-// result serves for both.
-__device__ __forceinline__ bool mbar_try_both(uint32_t bar0, uint32_t parity0, uint32_t bar1,
-                                              uint32_t parity1) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
-      "and.pred p, p, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
-      : "memory");
-  return ok != 0;
 }
 
 // The same wait with cluster-scope acquire: for a barrier that a thread of

@@ -9,15 +9,25 @@
 // warps read each block's accumulator and add it, times sa * sw, to their
 // own, while the tensor cores work on the next ones.
 //
-// A tile is 128 rows (256 on a CTA pair) x 256 weight rows.  What limits such
-// a kernel is the round trip accumulator ready -> read -> free -> next MMA,
-// some 1100 cycles long with 256 columns against the 512 that a block's MMAs
-// take, and the epilogue warps' own chain of waits.  So the 256 columns are
-// two halves of 128 that run apart from each other: an MMA warp, two TMEM
-// buffers and four epilogue warps each.
+// What limits such a kernel is the round trip accumulator ready -> read ->
+// free -> next MMA, some 1100 cycles long with 256 columns against the 512
+// that a block's MMAs take, and the epilogue warps' own chain of waits.  So the
+// 256 weight rows of a tile are two halves of 128 that run apart from each
+// other: an MMA warp, two TMEM buffers and four epilogue warps each.  Three
+// forms, chosen by rows per expert (launch_gemm_fp8):
+//   kOne   128 rows x 256 on one CTA;
+//   kPair  256 rows x 256 on two CTAs: half the weight bytes per CTA;
+//   kFew   32 rows x 256, for weight streaming: the MMAs are as tall as
+//          kOne's, but only 32 rows of A are loaded (by token, with gather4,
+//          where the rows are not sorted yet), one warp per half reads them,
+//          and where tiles are few a cluster shares out a tile's blocks and
+//          adds its sums over distributed shared memory.
+// 8192 rows of 4096 x 14336 (kPair): 445 us, 2.16 PFLOP/s.  9973 rows over 64
+// experts of 1408 x 2048, unevenly (kOne): 60 us.  16 rows of 4096 x 14336
+// (kFew): 20 us, the weights at 2.9 TB/s.
 //
 // One persistent CTA per SM (or pair of CTAs per two SMs), 384 threads:
-//   warp 0      TMA producer: A tile 128 x 128 and B rows (256, or this CTA's
+//   warp 0      TMA producer: A rows x 128 columns and B rows (256, or this CTA's
 //               128 of a pair) x 128 per block into a ring.  Without a pair,
 //               a row block of few rows is loaded by a lower box (8 to 128
 //               rows); the rest of the stage keeps what it held and feeds
@@ -29,7 +39,9 @@
 //               (two such groups), so that an epilogue warp's read is one
 //               conflict-free access;
 //   warps 4..11 epilogue: four warps per half, 32 TMEM lanes (rows) each, all
-//               128 columns of the half: 128 fp32 sums per thread.
+//               128 columns of the half: 128 fp32 sums per thread.  In kFew
+//               only the two warps of lanes 0..31 have rows; all eight finish
+//               them.
 // Registers move from warps 0..3 (72 each) to the epilogue (216): 128 * 72 +
 // 256 * 216 of the launch's 384 * 168.
 //
@@ -53,6 +65,7 @@
 // is bounded (common.cuh); after a timeout the epilogue runs through its loop
 // without waiting, so that no warp is left at a barrier.
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include <mutex>
 
@@ -62,6 +75,91 @@
 
 namespace moe {
 namespace {
+
+// The roles in the device error word, behind common.cuh's.
+enum : unsigned int {
+  SITE_FP8_PRODUCER = 1u << 18,
+  SITE_FP8_MMA = 1u << 19,
+  SITE_FP8_EPILOGUE = 1u << 20,
+  SITE_FP8_SCALES = 1u << 21,
+};
+static_assert(SITE_FP8_PRODUCER == SITE_PROBE << 1, "bits 8 to 17 are common.cuh's");
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Up to 4096 tries (0.1 ms and more) in a loop of four instructions, for waits
+// on a short loop's critical path: mbar_wait reads %globaltimer as soon as its
+// first try fails, and a try without success so far is the usual case there.
+// False is not final: go on with mbar_wait, out of the usual path.
+__device__ __forceinline__ bool mbar_try_loop(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n\t"
+      "TRY_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 4096;\n\t"
+      "@q bra TRY_%=;\n\t"
+      "DONE_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The same for a whole (converged) warp: lane 0 tries, a vote makes the result
+// uniform.
+__device__ __forceinline__ bool mbar_try_loop_warp(uint32_t bar, uint32_t parity, int lane) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred e, p, q;\n\t.reg .u32 n;\n\t"
+      "setp.eq.u32 e, %3, 0;\n\t"
+      "setp.ne.u32 p, 0, 0;\n\t"
+      "mov.u32 n, 0;\n\t"
+      "TRY_%=:\n\t"
+      "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.any.pred p, p, 0xffffffff;\n\t"
+      "@p bra.uni DONE_%=;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 4096;\n\t"
+      "@q bra.uni TRY_%=;\n\t"
+      "DONE_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(static_cast<uint32_t>(lane))
+      : "memory");
+  return ok != 0;
+}
+
+// Tries two barriers at once: their latencies overlap, and one branch on the
+// result serves for both.
+__device__ __forceinline__ bool mbar_try_both(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                              uint32_t parity1) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
+      : "memory");
+  return ok != 0;
+}
 
 constexpr int BM = 128;                        // rows per CTA
 constexpr int BK = 128;                        // bytes = e4m3 values = one scale block
@@ -288,8 +386,7 @@ __device__ __forceinline__ void tma_gather4(const CUtensorMap* map, uint64_t* ba
 }
 
 // Two neighbouring columns in one 64-bit register.  fma.rn.f32x2 does the work
-// of two FMAs in one issue slot (at their rate, two cycles): the epilogue's
-// issue slots are scarce.
+// of two FMAs in one issue slot (at their rate, two cycles).
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 both(float s) {
   f32x2 r;
@@ -373,13 +470,17 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-// The power of two that brings a block with largest magnitude amax to the top
-// of fp16's range (its inverse is what is stored); 1 for zeros, infinities
-// and NaN.
+// The power of two that brings a block with largest finite magnitude amax to
+// the top of fp16's range (its inverse is what is stored); 1 for zeros.
 __device__ __forceinline__ float f16_scale(float amax) {
   const int e = static_cast<int>(__float_as_uint(amax) >> 23);         // biased exponent, amax >= 0
-  if (e == 0 || e == 255) return 1.f;
+  if (e == 0) return 1.f;
   return __uint_as_float(static_cast<uint32_t>(min(max(127 + 14 - (e - 127), 1), 254)) << 23);
+}
+// |x|, or 0 for infinities and NaN: they stay what they are whatever the scale.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= FLT_MAX ? a : 0.f;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -435,7 +536,8 @@ __device__ __forceinline__ void finish_row(const Params& p, const Tile& tl, int 
       const float4 v = c ? v1 : v0;
       if constexpr (EPI == kOutF16) {
         const bool in = col < p.n_out;           // columns past it: another expert's, not to be looked at
-        float m = in ? fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))) : 0.f;
+        float m = in ? fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)),
+                             fmaxf(finite_abs(v.z), finite_abs(v.w))) : 0.f;
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float s = f16_scale(m);
@@ -929,7 +1031,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float2 f = unpack(acc[c][j]);
-              if (col + 2 * j < p.n_out) m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+              if (col + 2 * j < p.n_out) m = fmaxf(m, fmaxf(finite_abs(f.x), finite_abs(f.y)));
             }
             s = f16_scale(m);
             if (rvalid && col < p.n_out)

@@ -421,6 +421,28 @@ def test_experts_unused_slots_and_repeats(T):
     assert (run_experts(args) == 0).all()
 
 
+@pytest.mark.parametrize("T", [2, 300, 1600])
+def test_experts_infinite_column(T):
+    """A column whose sum passes fp32's range is infinite; its neighbours keep their large finite values."""
+    D, F = 256, 128
+    x, xs, sel, w, gu, gus, dn, dns = make_experts(T, D, F, 2, 1, seed=5)
+    x.copy_(torch.ones_like(x, dtype=torch.float32).to(F8))
+    xs.fill_(1.0)
+    gu.copy_(torch.ones_like(gu, dtype=torch.float32).to(F8))
+    gus.fill_(1.0 / 32)                          # gate = up = 8: h about 64 in every column
+    dn.copy_(torch.full_like(dn, 2.0 ** -6, dtype=torch.float32).to(F8))
+    dn[:, 17] = 448.0
+    dns.fill_(2.0 ** 110)
+    w.fill_(1.0)
+    out = run_experts([x, xs, sel, w, gu, gus, dn, dns])
+    h = 8 / (1 + torch.exp(torch.tensor(-8.0, dtype=torch.float64))) * 8
+    assert (out[:, 17] == INF).all()             # 128 * 64 * 448 * 2^110 > 2^128
+    rest = out[:, torch.arange(D, device="cuda") != 17].double()
+    want = float(h) * 128 * 2.0 ** 104
+    # the intermediate's e4m3 (2^-4), fp16 and bf16
+    assert ((rest / want - 1).abs() <= 2.0 ** -4 + 2.0 ** -7).all()
+
+
 def test_experts_streams_graph_and_shared_workspace():
     """Another stream; two captured calls that share a workspace, replayed with new inputs."""
     args, other = make_experts(24, 256, 384, 8, 2, seed=1), make_experts(300, 256, 384, 8, 2, seed=2)
