@@ -299,6 +299,7 @@ MOE_API moe_status_t moe_ffn_forward_noalloc(const void* x, const void* router,
  * residual, sum_out, out, and the pair out_fp8 and scales may be NULL; one of
  * out and out_fp8 is required.  sum_out and out may be x or residual
  * themselves (in place), but not each other; no other overlap is allowed.
+ * h^2 is summed in fp32: a row whose sum passes its range gives zeros.
  * Any D up to MOE_NORM_MAX_D (vector loads when D is a multiple of 8).
  */
 #define MOE_NORM_MAX_D 32768
@@ -390,8 +391,9 @@ MOE_API moe_status_t moe_gemm_fp8(const void* a, const float* a_scales, const vo
  * weight is not read as a number (padded tokens get a row of zeros).  The
  * same expert twice in a token counts twice.  The intermediate is rounded to
  * 8 bits once, each expert's output to block-scaled fp16 once, the weighted
- * sum (fp32, in slot order) to bf16 once.  D and F must be multiples of 16.  With the stage
- * profiler on the call is recorded like a forward (no router stage).
+ * sum (fp32, in slot order) to bf16 once.  D and F must be multiples of 16,
+ * D at most 65535 * 1024.  With the stage profiler on the call is recorded
+ * like a forward (no router stage).
  */
 MOE_API size_t moe_experts_workspace_size_fp8(int64_t T, int64_t D, int64_t F, int E, int K);
 MOE_API moe_status_t moe_experts_forward_fp8(

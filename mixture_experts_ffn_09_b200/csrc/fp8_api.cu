@@ -227,7 +227,8 @@ moe_status_t check_experts(int64_t T, int64_t D, int64_t F, int E, int K) {
   if (K < 1 || K > E) return fail_status(MOE_ERR_INVALID_ARG, "top_k=%d outside [1, E=%d]", K, E);
   if (E > MOE_MAX_EXPERTS)
     return fail_status(MOE_ERR_SHAPE, "E=%d exceeds MOE_MAX_EXPERTS=%d", E, MOE_MAX_EXPERTS);
-  if (T > INT_MAX || T * K > INT_MAX - 128 || D > INT_MAX / 2 || F > INT_MAX / 2 ||
+  // D: the combine's grid has a row of CTAs per 1024 columns, 65535 of them at most
+  if (T > INT_MAX || T * K > INT_MAX - 128 || D > 65535LL * 1024 || F > INT_MAX / 2 ||
       static_cast<int64_t>(E) * 2 * F + 256 > INT_MAX || static_cast<int64_t>(E) * D + 256 > INT_MAX)
     return fail_status(MOE_ERR_SHAPE, "sizes exceed 32-bit indexing");
   if (D % 16 != 0 || F % 16 != 0)

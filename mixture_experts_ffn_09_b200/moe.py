@@ -783,7 +783,11 @@ class MoEBlockFP8:
     (D,) the input is normed first; ``forward(x, residual)`` then returns the
     block's output, and ``residual_`` holds x + residual.  Routing options are
     those of :func:`select_experts`.  Keeps ``router_logits_``,
-    ``selected_experts_`` and ``routing_weights_`` of the last call."""
+    ``selected_experts_`` and ``routing_weights_`` of the last call.
+
+    Calls may overlap on several streams: every call takes its buffers, the
+    workspace too, from the allocator's pool of its stream (of the graph,
+    while one is captured), and none is kept for the next call."""
 
     def __init__(self, router, gate_up_proj, down_proj, top_k: int = 2, norm_topk_prob: bool = True,
                  norm_weight=None, eps: float = 1e-6, router_bias=None, **routing):
@@ -805,7 +809,6 @@ class MoEBlockFP8:
         quantize_fp8(gate_up_proj.view(E, 2, F, D), self.gate_up_proj.view(E, 2, F, D),
                      self.gate_up_scales, QUANT_BLOCK)
         quantize_fp8(down_proj, self.down_proj, self.down_scales, QUANT_BLOCK)
-        self._ws = None
         self.residual_ = self.router_logits_ = self.selected_experts_ = self.routing_weights_ = None
 
     @property
@@ -816,6 +819,9 @@ class MoEBlockFP8:
         import torch
         if residual is not None and self.norm_weight is None:
             raise ValueError("a residual needs norm_weight")
+        if stream is not None:                 # buffers of that stream's pool
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+                return self.forward(x, residual)
         E, F, D = int(self.down_proj.shape[0]), int(self.down_proj.shape[-1]), int(x.shape[-1])
         T, K = _rows(x), self.top_k
         new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
@@ -824,23 +830,19 @@ class MoEBlockFP8:
             self.residual_ = torch.empty_like(x) if residual is not None else x
             y = torch.empty_like(x)
             add_rmsnorm(x, self.norm_weight, self.eps, residual,
-                        self.residual_ if residual is not None else None, y, x8, xs, stream)
+                        self.residual_ if residual is not None else None, y, x8, xs)
             x = y
         else:
-            quantize_fp8(x.view(T, D), x8.view(T, D), xs, 1, stream)
+            quantize_fp8(x.view(T, D), x8.view(T, D), xs, 1)
         self.router_logits_ = new((T, E), torch.float32)
         self.selected_experts_ = new((T, K), torch.int64)
         self.routing_weights_ = new((T, K), torch.float32)
         route_groups(x, self.router, K, self.norm_topk_prob, self.router_logits_,
-                     self.selected_experts_, self.routing_weights_, self.router_bias, stream=stream,
-                     **self.routing)
-        need = experts_workspace_size_fp8(T, D, F, E, K)
-        if self._ws is None or self._ws.numel() < need or self._ws.device != x.device:
-            self._ws = new(max(need, 1), torch.uint8)
+                     self.selected_experts_, self.routing_weights_, self.router_bias, **self.routing)
+        ws = new(max(experts_workspace_size_fp8(T, D, F, E, K), 1), torch.uint8)
         out = new(x.shape, torch.bfloat16)
         experts_forward_fp8(x8, xs, self.selected_experts_, self.routing_weights_, self.gate_up_proj,
-                            self.gate_up_scales, self.down_proj, self.down_scales, out, self._ws,
-                            stream)
+                            self.gate_up_scales, self.down_proj, self.down_scales, out, ws)
         return out
 
     __call__ = forward

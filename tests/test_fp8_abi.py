@@ -107,7 +107,7 @@ EXPERTS = dict(x=P, xs=P, sel=P, rw=P, gu=P, gus=P, dn=P, dns=P, out=P, T=4, D=6
 @pytest.mark.parametrize("change,want", [
     (dict(T=0), moe.MOE_ERR_INVALID_ARG), (dict(F=0), moe.MOE_ERR_INVALID_ARG), (dict(K=9), moe.MOE_ERR_INVALID_ARG),
     (dict(K=0), moe.MOE_ERR_INVALID_ARG), (dict(E=300), moe.MOE_ERR_SHAPE), (dict(T=2 ** 30, K=2), moe.MOE_ERR_SHAPE),
-    (dict(F=2 ** 28, E=8), moe.MOE_ERR_SHAPE), (dict(D=72), moe.MOE_ERR_ALIGNMENT), (dict(F=8), moe.MOE_ERR_ALIGNMENT),
+    (dict(F=2 ** 28, E=8), moe.MOE_ERR_SHAPE), (dict(D=2 ** 26), moe.MOE_ERR_SHAPE), (dict(D=72), moe.MOE_ERR_ALIGNMENT), (dict(F=8), moe.MOE_ERR_ALIGNMENT),
     (dict(x=None), moe.MOE_ERR_INVALID_ARG), (dict(dns=None), moe.MOE_ERR_INVALID_ARG), (dict(out=MIS), moe.MOE_ERR_ALIGNMENT),
     (dict(ws=None), moe.MOE_ERR_WORKSPACE), (dict(nb=64), moe.MOE_ERR_WORKSPACE), (dict(ws=MIS), moe.MOE_ERR_ALIGNMENT)])
 def test_experts_refusals(L, change, want):

@@ -543,3 +543,49 @@ def test_block(T, D, F, E, K, residual):
     assert (out.double() - want).norm() <= 2.0 ** -3 * want.norm()
     again = blk(x, r) if residual else blk(x)
     assert torch.equal(out, again)
+
+
+def make_block(E=16, D=256, F=384):
+    bf = torch.bfloat16
+    return moe.MoEBlockFP8(randn(E, D, seed=1, std=0.1).to(bf), randn(E, 2 * F, D, seed=2, std=D ** -0.5).to(bf),
+                           randn(E, D, F, seed=3, std=F ** -0.5).to(bf), top_k=4, norm_weight=(1 + 0.1 * randn(D, seed=4)).to(bf),
+                           score="sigmoid", groups=4, top_groups=2)
+
+
+def test_block_on_streams_at_once():
+    """One block on two streams (an object and a raw handle) at the same time."""
+    blk = make_block()
+    xs = [randn(T, 256, seed=T).bfloat16() for T in (40, 700)]
+    want = [blk(x, x) for x in xs]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):
+        got = [blk(x, x, stream=st if i else st.cuda_stream) for i, (x, st) in enumerate(zip(xs, s))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_block_captured_twice():
+    """Two graphs of one block, replayed at the same time with an eager call, and again with other inputs."""
+    blk = make_block()
+    xs = [randn(T, 256, seed=T).bfloat16() for T in (40, 700, 300)]
+    want = [blk(x, x) for x in xs]
+    graphs, outs = [], []
+    for x in xs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(blk(x, x))
+        graphs.append(g)
+    s = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, st in zip(graphs, s):
+            with torch.cuda.stream(st):
+                g.replay()
+        eager = blk(xs[2], xs[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip([*outs, eager], want))
+    xs[0].copy_(randn(40, 256, seed=99))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], blk(xs[0], xs[0]))
