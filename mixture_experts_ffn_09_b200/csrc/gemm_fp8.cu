@@ -184,7 +184,8 @@ struct Cfg {
   static constexpr int A_BYTES = (MODE == kFew ? TILE_M : BM) * BK;
   static constexpr int B_BYTES = (MODE == kPair ? BN / 2 : BN) * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int QUADS = MODE == kFew ? 1 : 4;   // groups of 32 TMEM lanes with rows
+  static constexpr int QUADS = MODE == kFew ? 1 : 4;   // groups of 32 rows
+  static constexpr int READERS = MODE == kFew ? 2 : 4; // warps that read a half's accumulators
 };
 
 enum { kOutBf16 = 0, kOutF32 = 1, kSiluQuant = 2, kOutF16 = 3 };
@@ -245,9 +246,10 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<kOne>() <= 227 * 1024 && smem_bytes<kPair>() <= 227 * 1024 &&
               smem_bytes<kFew>() <= 227 * 1024, "shared memory");
-// An M = 128 MMA of kFew reads past the stage's 32 rows into what follows in
-// shared memory (rows that are never looked at): it has to be there.
-static_assert(Cfg<kFew>::STAGES * Cfg<kFew>::B_BYTES >= BM * BK, "A reads stay inside the ring");
+// An M = 128 MMA of kFew reads 96 rows around the stage's 32, up to 32 of them
+// in front (accumulator rows that are never looked at): they have to be there.
+static_assert(sizeof(Tail<kFew>) >= 96 * BK && Cfg<kFew>::STAGES * Cfg<kFew>::B_BYTES >= 32 * BK,
+              "A reads stay inside this CTA's shared memory");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -572,8 +574,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   // 1024-byte aligned by its address in the shared window: the same offset in
   // both CTAs of a pair
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + STAGES * A_BYTES;
+  uint8_t* sA = MODE == kFew ? smem + STAGES * C::B_BYTES : smem;
+  uint8_t* sB = MODE == kFew ? smem : smem + STAGES * A_BYTES;
   Tail<MODE>* st = reinterpret_cast<Tail<MODE>*>(smem + STAGES * C::STAGE_BYTES);
 
   constexpr int BN_OUT = EPI == kSiluQuant ? 128 : 256;
@@ -597,12 +599,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int a = 0; a < 2; ++a) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&st->tfull[a][b], 1);
-        mbar_init(&st->tempty[a][b], (PAIR ? 2 : 1) * C::QUADS);
+        mbar_init(&st->tempty[a][b], (PAIR ? 2 : 1) * C::READERS);
       }
-      mbar_init(&st->xfull[a], 2 * C::QUADS);
+      mbar_init(&st->xfull[a], 2 * C::READERS);
       if (a == 0) mbar_init(&st->xempty, EPI_WARPS);
       mbar_init(&st->sfull[a], 1);
-      mbar_init(&st->sempty[a], 2 * C::QUADS);
+      mbar_init(&st->sempty[a], 2 * C::READERS);
       mbar_init(&st->mma_done[a], 1);
     }
     st->abort = 0;
@@ -764,7 +766,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int half = warp - 1;
     constexpr uint32_t idesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BH);
     if (rank == 0 && elect_one()) {
-      const uint64_t da = sw128_kmajor_desc(smem_u32(sA));
+      // kFew: the second half's rows become accumulator rows 32..63, which other
+      // warps can read
+      const uint64_t da = sw128_kmajor_desc(smem_u32(sA) - (MODE == kFew ? half * 32 * BK : 0));
       const uint64_t db = sw128_kmajor_desc(smem_u32(sB) + half * (PAIR ? 64 : 128) * BK);
       const uint32_t d0 = tmem + half * 2 * BH;
       const uint32_t full0 = smem_u32(&st->full[0]), tempty0 = smem_u32(&st->tempty[half][0]);
@@ -864,11 +868,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3;                   // TMEM lanes this warp may access
-    const int half = (warp - EPI_WARP0) >> 2;
-    const int r = quad * 32 + lane;              // row of this CTA's 128
+    const int sub = (warp - EPI_WARP0) >> 2;
+    // kFew: half h has its rows in lanes 32 h .. 32 h + 31, whose two warps take
+    // the columns of a weight block each
+    const int half = MODE == kFew ? quad : sub;
+    const int r = MODE == kFew ? lane : quad * 32 + lane;     // row of this CTA's
     // the buffer to read next: its columns, its barriers (8 bytes apart at
     // multiples of 16) and the parity of its turn
-    uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 2 * BH;
+    uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 2 * BH + (MODE == kFew ? 64 * sub : 0);
     uint32_t tfull = smem_u32(&st->tfull[half][0]);
     uint32_t tempty = PAIR ? map_to_rank0(&st->tempty[half][0]) : smem_u32(&st->tempty[half][0]);
     uint32_t par = 0;
@@ -885,17 +892,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&st->xempty);
     };
-    if (quad >= C::QUADS && split == 1)
+    const bool reads = MODE != kFew || quad < 2;
+    if (!reads && split == 1)
       for (int t = worker, m = 0; t < total; t += workers, ++m) few_rows(tile_of(t), m);
-    for (int t = quad < C::QUADS ? worker : total; t < total; t += workers, ++n) {
+    for (int t = reads ? worker : total; t < total; t += workers, ++n) {
       const Tile tl = tile_of(t);
       const int rows = min(tl.rows - static_cast<int>(rank) * BM, MODE == kFew ? C::TILE_M : BM);
-      const bool live = quad * 32 < rows;        // warp-uniform
+      const bool live = MODE == kFew || quad * 32 < rows;      // warp-uniform
       const bool rvalid = r < rows;
       const int grow = tl.row0 + static_cast<int>(rank) * BM + (rvalid ? r : 0);
-      f32x2 acc[2][32];                          // 64 columns of each weight block, in pairs
+      constexpr int WB = MODE == kFew ? 1 : 2;
+      f32x2 acc[WB][32];                         // 64 columns of each weight block, in pairs
 #pragma unroll
-      for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0ull;
+      for (int c = 0; c < WB; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[c][j] = 0ull;
       // Each block's accumulator, times a * w, onto the sums.  A scheduler has
       // two such warps, so what counts is the length of this chain: few
       // branches, one lane's arrivals as predicated instructions, the next
@@ -919,19 +930,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld32(src, v0);
             tmem_ld32(src + 32, v1);
           }
-          const f32x2 s0 = both(a * w.x), s1 = both(a * w.y);
+          const f32x2 s0 = both(a * (MODE == kFew && sub ? w.y : w.x)), s1 = both(a * w.y);
           const int kn = min(k + 1, SCALE_KB - 1);
           a = sa[kn * kRows];
           w = sw[kn];
           if (live) {
             tmem_ld_wait();
+            if constexpr (MODE != kFew) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma2(acc[0][j], v0[2 * j], v0[2 * j + 1], s0);
-            tmem_ld32(src + 64, v0);
+              for (int j = 0; j < 16; ++j) fma2(acc[0][j], v0[2 * j], v0[2 * j + 1], s0);
+              tmem_ld32(src + 64, v0);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma2(acc[0][16 + j], v1[2 * j], v1[2 * j + 1], s0);
-            tmem_ld32(src + 96, v1);
-            tmem_ld_wait();
+              for (int j = 0; j < 16; ++j) fma2(acc[0][16 + j], v1[2 * j], v1[2 * j + 1], s0);
+              tmem_ld32(src + 96, v1);
+              tmem_ld_wait();
+            }
           }
           // all of it is in registers, of every lane: the buffer is free
           tc_fence_before();
@@ -941,10 +954,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           tfull ^= 8u;
           tempty ^= 8u;
           if (live) {
+            const f32x2 s = MODE == kFew ? s0 : s1;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma2(acc[1][j], v0[2 * j], v0[2 * j + 1], s1);
+            for (int j = 0; j < 16; ++j) fma2(acc[WB - 1][j], v0[2 * j], v0[2 * j + 1], s);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma2(acc[1][16 + j], v1[2 * j], v1[2 * j + 1], s1);
+            for (int j = 0; j < 16; ++j) fma2(acc[WB - 1][16 + j], v1[2 * j], v1[2 * j + 1], s);
           }
         }
         __syncwarp();
@@ -956,14 +970,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         // finish them, a warp per row: on this warp alone, 64 lots of silu and
         // a row of stores took 4 us a tile.
         if (n > 0) warp_wait(&st->xempty, (n - 1) & 1u, lane, abort, p.err, SITE_FP8_EPILOGUE);
-        float* dst = &st->part[r][half * 64];
+        float* dst = &st->part[r][sub * 128 + half * 64];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 x = unpack(acc[c][2 * j]), y = unpack(acc[c][2 * j + 1]);
-            *reinterpret_cast<float4*>(dst + c * 128 + 4 * j) = make_float4(x.x, x.y, y.x, y.y);
-          }
+        for (int j = 0; j < 16; ++j) {
+          const float2 x = unpack(acc[0][2 * j]), y = unpack(acc[0][2 * j + 1]);
+          *reinterpret_cast<float4*>(dst + 4 * j) = make_float4(x.x, x.y, y.x, y.y);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->xfull[0]);
         if (split == 1) few_rows(tl, n);
@@ -1023,7 +1035,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr int kBytes = EPI == kOutF32 ? 4 : 2;
         uint8_t* out = static_cast<uint8_t*>(p.out) + static_cast<size_t>(tl.row0 + row_in) * p.n_out * kBytes;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < WB; ++c) {
           float s = 1.f;
           if constexpr (EPI == kOutF16) {        // 64 columns in this thread: a block
             const int col = tl.n_blk * 256 + c * 128 + half * 64;
