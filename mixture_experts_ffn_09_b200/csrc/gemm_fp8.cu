@@ -1191,6 +1191,13 @@ cudaError_t resident_clusters(int size, int* out) {
   return cudaSuccess;
 }
 
+// The most tiles that M rows of E experts can make, whatever the offsets.
+long long tile_bound(long long M, int E, int tile_m, long long n_tiles) {
+  const long long touched = M < E ? M : E;
+  if (E == 1) return (M + tile_m - 1) / tile_m * n_tiles;
+  return (M <= tile_m ? touched : M / tile_m + touched) * n_tiles;
+}
+
 template <int EPI, int MODE>
 cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, Params p, cudaStream_t s) {
   int workers = 0;
@@ -1199,9 +1206,7 @@ cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, Params p, cudaStrea
   const int bn_out = EPI == kSiluQuant ? 128 : 256;
   const long long n_tiles = (p.n_out + bn_out - 1) / bn_out;
   constexpr int tile_m = Cfg<MODE>::TILE_M;
-  const long long touched = p.M < p.E ? p.M : p.E;
-  const long long bound = p.M <= tile_m ? touched * n_tiles
-                                        : (static_cast<long long>(p.M) / tile_m + touched) * n_tiles;
+  const long long bound = tile_bound(p.M, p.E, tile_m, n_tiles);
   if (MODE == kPair) {
     const int pairs = static_cast<int>(bound < workers ? bound : workers);
     return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(2 * pairs), dim3(THREADS), smem_bytes<MODE>(), s, false,
@@ -1223,7 +1228,7 @@ cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, Params p, cudaStrea
   // With at most one row block per expert on average (weight streaming), size
   // the grid so that every CTA takes the same number of tiles.
   long long tiles = bound;
-  if (p.M <= static_cast<long long>(tile_m) * p.E) tiles = touched * n_tiles;
+  if (p.M <= static_cast<long long>(tile_m) * p.E) tiles = (p.M < p.E ? p.M : p.E) * n_tiles;
   const long long waves = (tiles + workers - 1) / workers;
   const int grid = static_cast<int>((tiles + waves - 1) / waves);
   return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(grid), dim3(THREADS), smem_bytes<MODE>(), s, false, 1, a,
@@ -1263,15 +1268,15 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   p.out_scales = gated ? g.q_scales : g.f16_scales;
   p.err = g.err;
   // By the rows of an expert on average.  Us a product, 32 rows | one CTA | pair:
-  // 16 experts of 2048 x 2048, 24 rows each: 19 | 19 | 27, 32 rows: 27 | 20 | 27,
+  // 16 experts of 2048 x 2048, 24 rows each: 19 | 19 | 27, 32 rows: 23 | 20 | 27,
   // 512 rows: 138 | 57 | 58; 64 experts of 2816 x 2048, 512 rows each: one CTA
   // 244, pair 257 (half a pair tile of padding per expert); 8192 rows of 4096 x
-  // 14336: one CTA 470, pair 435.  Where one CTA per tile would leave half the
-  // SMs idle, the 32-row form shares tiles out: 64 rows of 4096 x 4096: 17 | 21,
-  // 128 rows: 21 | 21.
-  const long long few_tiles = ((g.M + BM - 1) / BM + (g.E > 1 ? g.E : 0)) * ((g.N + 255) / 256);
-  int mode = g.M <= 24LL * g.E || (g.M <= 96LL * g.E && few_tiles * 2 <= num_sms()) ? kFew : kOne;
-  if (g.M >= 768LL * g.E) mode = kPair;
+  // 14336: one CTA 470, pair 435.  Where even tiles of 32 rows leave half the
+  // SMs idle, that form shares each one out: 64 rows of 4096 x 4096: 14 | 21 | 21,
+  // 128 rows: 19 | 22 | 22, 2000 rows of 256 x 7168: 19 | 31 | 32.
+  const long long few_tiles = tile_bound(g.M, g.E, Cfg<kFew>::TILE_M, gated ? blocks : (g.N + 255) / 256);
+  int mode = g.M >= 768LL * g.E ? kPair : kOne;
+  if (g.M <= 24LL * g.E || few_tiles * 2 <= num_sms()) mode = kFew;
   if (g.gather) mode = kFew;                     // the only form that fetches rows by token
   AMaps ma;
   CUtensorMap mb;
