@@ -198,6 +198,9 @@ struct Params {
   const int* offsets;    // (E + 1) first row of each expert, or null: one expert, all M rows
   const int* perm;       // row -> (token, slot): the row of the scales is perm[row] / slots; or null
   int slots;
+  const int64_t* selected;   // set (kFew, gated, M <= THREADS): every CTA sorts the M slots itself
+  int* offsets_out;          // and the first one writes offsets and the slots' rows
+  int* pos_out;
   int gather;            // 1: the rows of A are fetched by token too (its map is one row high)
   int M, E;
   int n_out;             // output columns
@@ -233,6 +236,7 @@ struct Tail {
   int off[kMaxExperts + 1];
   alignas(16) float amax[2][2][MODE == kFew ? 1 : BM];   // [tile parity][half][row]
   alignas(16) float sa[2][SCALE_KB][32 * Cfg<MODE>::QUADS];
+  int perm[MODE == kFew ? THREADS : 1];
   // kFew: the tile's sums, a row of 256 columns after the other; 16 bytes more
   // per row keep row-per-lane accesses free of bank conflicts
   alignas(16) float part[MODE == kFew ? 32 : 1][kPartStride];
@@ -610,28 +614,65 @@ __global__ void __launch_bounds__(THREADS, 1)
     st->abort = 0;
     mbar_fence_init();
   }
+  // A small batch's slots are sorted by expert here, a thread per slot, by every
+  // CTA for itself (stable: by slot): one launch less, 4 us.
+  constexpr bool kSorts = EPI == kSiluQuant && MODE == kFew;
+  const bool sorts = kSorts && p.selected != nullptr;
+  int* count = reinterpret_cast<int*>(st->part);                   // an expert's slots
+  int* warp_count = count + kMaxExperts;                           // of a warp's 32, [warp][expert]
+  int expert = -1, rank_in = 0;
+  if constexpr (kSorts) {
+    if (sorts) {
+      const int64_t v = threadIdx.x < p.M ? __ldg(p.selected + threadIdx.x) : -1;
+      if (v >= 0 && v < E) expert = static_cast<int>(v);
+      for (int i = threadIdx.x; i < (1 + THREADS / 32) * kMaxExperts; i += THREADS) count[i] = 0;
+      __syncthreads();
+      const unsigned int same = __match_any_sync(0xffffffffu, expert);
+      rank_in = __popc(same & ((1u << lane) - 1u));
+      if (expert >= 0 && rank_in == 0) {
+        warp_count[warp * kMaxExperts + expert] = __popc(same);
+        atomicAdd(&count[expert], __popc(same));                   // integers: the order is free
+      }
+      __syncthreads();
+    }
+  }
   if (warp == 2) {
-    // The tile table.  Offsets are device data: kept within [0, M] and in
-    // order (a running maximum), so that no address below depends on their
-    // being right.  A lane takes eight experts.
+    // The tile table, a lane for eight experts.
     int o[9];
+    if (sorts) {
+      int sum = 0;
 #pragma unroll
-    for (int i = 0; i < 9; ++i) {
-      const int e = lane * 8 + i;
-      o[i] = p.offsets && e <= E ? min(max(__ldg(p.offsets + e), 0), p.M) : (e == 0 ? 0 : p.M);
-      if (i > 0) o[i] = max(o[i], o[i - 1]);
-    }
-    int high = o[8];                             // over the lanes before
+      for (int i = 0; i < 8; ++i) sum += count[lane * 8 + i];
+      int incl = sum;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, high, d);
-      if (lane >= d) high = max(high, v);
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      o[0] = incl - sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i + 1] = o[i] + count[lane * 8 + i];
+    } else {
+      // Offsets are device data: kept within [0, M] and in order (a running
+      // maximum), so that no address below depends on their being right.
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        const int e = lane * 8 + i;
+        o[i] = p.offsets && e <= E ? min(max(__ldg(p.offsets + e), 0), p.M) : (e == 0 ? 0 : p.M);
+        if (i > 0) o[i] = max(o[i], o[i - 1]);
+      }
+      int high = o[8];                           // over the lanes before
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, high, d);
+        if (lane >= d) high = max(high, v);
+      }
+      high = __shfl_up_sync(0xffffffffu, high, 1);
+      if (lane == 0) high = 0;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) o[i] = max(o[i], high);
     }
-    high = __shfl_up_sync(0xffffffffu, high, 1);
-    if (lane == 0) high = 0;
     int tiles[8], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 9; ++i) o[i] = max(o[i], high);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       tiles[i] = lane * 8 + i < E ? (o[i + 1] - o[i] + C::TILE_M - 1) / C::TILE_M * n_tiles : 0;
@@ -663,6 +704,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (warp == 0 && lane == 0) tma_prefetch_desc(&tmB);
   if (warp == 1) tmem_get<PAIR>(&st->tmem_base);
+  if constexpr (kSorts) {
+    if (sorts) {
+      __syncthreads();
+      int row = -1;
+      if (expert >= 0) {
+        row = st->off[expert] + rank_in;
+        for (int w = 0; w < warp; ++w) row += warp_count[w * kMaxExperts + expert];
+        st->perm[row] = threadIdx.x;
+      }
+      if (blockIdx.x == 0) {
+        if (threadIdx.x < p.M) p.pos_out[threadIdx.x] = row;
+        if (threadIdx.x <= E) p.offsets_out[threadIdx.x] = st->off[threadIdx.x];
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();      // the leader's barriers exist before the peer uses them
@@ -671,6 +727,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = st->tmem_base;
   const int total = st->total_tiles;
   volatile int* abort = &st->abort;
+  auto slot_of = [&](int row) { return sorts ? st->perm[row] : __ldg(p.perm + row); };
   auto tile_of = [&](int t) { return decode_tile(st->tile_start, st->off, E, n_tiles, C::TILE_M, t); };
 
   // (each register split dominates its warps' code, so that the compiler
@@ -712,7 +769,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int tok[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)              // past the last row: that row again
-          tok[i] = __ldg(p.perm + tl.row0 + min(4 * lane + i, rows - 1)) / p.slots;
+          tok[i] = slot_of(tl.row0 + min(4 * lane + i, rows - 1)) / p.slots;
         for (int kb = kb_lo; kb < kb_hi; ++kb) {
           if (!warp_wait(&st->empty[stage], phase ^ 1u, lane, abort, p.err, SITE_FP8_PRODUCER)) {
             ok = false;
@@ -817,7 +874,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int h = 0; h < C::QUADS; ++h) {       // past the last row: that row again
         const int grow = tl.row0 + min(static_cast<int>(rank) * BM + h * 32 + lane, tl.rows - 1);
-        sa[h] = p.sa + static_cast<size_t>(p.perm ? __ldg(p.perm + grow) / p.slots : grow) * p.num_kb;
+        sa[h] = p.sa + static_cast<size_t>(p.perm ? slot_of(grow) / p.slots : grow) * p.num_kb;
       }
     };
     auto fetch = [&](int k0) {                   // past the last block: that block again
@@ -1246,12 +1303,17 @@ cudaError_t launch_mode(const GemmFp8Args& g, const AMaps& a, const CUtensorMap&
 
 }  // namespace
 
+bool gemm_fp8_sorts(int64_t slots, bool gather) { return gather && slots <= THREADS; }
+
 cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   const bool gated = g.q_scales != nullptr;
   Params p{};
   p.offsets = g.offsets;
   p.perm = g.perm;
   p.slots = g.slots;
+  p.selected = g.selected;
+  p.offsets_out = g.offsets_out;
+  p.pos_out = g.pos_out;
   p.gather = g.gather ? 1 : 0;
   p.M = g.M;
   p.E = g.E;

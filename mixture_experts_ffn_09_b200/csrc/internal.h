@@ -185,7 +185,10 @@ cudaError_t launch_select_experts(const SelectArgs& a, cudaStream_t s);
 // The block-scaled grouped GEMM.  With q_scales set it is the gated form:
 // the weights hold N gate rows, then N up rows per expert, and out gets the
 // e4m3 blocks of silu(gate) * up.  With perm set the row of A's scales is
-// perm[row] / slots, and with gather that of A itself too.
+// perm[row] / slots, and with gather that of A itself too.  With selected set
+// (gated and gather, where gemm_fp8_sorts) the kernel sorts the M slots itself:
+// offsets and perm are not read, offsets_out (E + 1) and pos_out (M; -1: an
+// unused slot) are written.
 struct GemmFp8Args {
   const void* a;           // (a_rows, K) e4m3
   const float* a_scales;   // (rows, ceil(K / 128))
@@ -194,6 +197,9 @@ struct GemmFp8Args {
   const int* offsets;      // (E + 1) or null (E = 1, all M rows)
   const int* perm;
   int slots;
+  const int64_t* selected;
+  int* offsets_out;
+  int* pos_out;
   bool gather;
   int a_rows, M, E, N, K;
   void* out;
@@ -203,6 +209,7 @@ struct GemmFp8Args {
   unsigned int* err;
 };
 cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s);
+bool gemm_fp8_sorts(int64_t slots, bool gather);
 
 // out[t, :] = sum_k w[t, k] * Y[pos[t, k], :] in bf16, Y in fp16 with a scale
 // per row and 64 columns; fp32 sum in k order; slots with pos < 0 add nothing.
