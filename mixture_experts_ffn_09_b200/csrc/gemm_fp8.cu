@@ -231,7 +231,7 @@ struct Tail {
   uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort;
-  int total_tiles;
+  int total_tiles, workers;
   int tile_start[kMaxExperts + 1];
   int off[kMaxExperts + 1];
   alignas(16) float amax[2][2][MODE == kFew ? 1 : BM];   // [tile parity][half][row]
@@ -589,8 +589,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   // with split blocks one tile only: the grid covers every possible one
   const int split = MODE == kFew ? p.split : 1;
   const int share = MODE == kFew && split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int most = PAIR ? gridDim.x >> 1 : split > 1 ? 1 << 30 : gridDim.x;
   const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x / split;
-  const int workers = PAIR ? gridDim.x >> 1 : split > 1 ? 1 << 30 : gridDim.x;
   const int kb_lo = share * p.num_kb / split, kb_hi = (share + 1) * p.num_kb / split;
   const int E = p.E;
   const int n_tiles = (p.n_out + BN_OUT - 1) / BN_OUT;
@@ -695,7 +695,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       at += tiles[i];
     }
     if (lane == 31) {
-      st->total_tiles = at;
+      // With as many waves as all workers would need, as few of them as get the
+      // same number of tiles each: the rest would only share the first waves'
+      // bandwidth (a decode step over 64 experts: 97 us, with all of them 99).
+      const int waves = max(1, (at + most - 1) / most);
+      const int workers = split > 1 ? most : max(1, (at + waves - 1) / waves);
+      st->workers = workers;
+      st->total_tiles = worker < workers ? at : 0;         // 0: none for this CTA
       if (E == kMaxExperts) {
         st->off[E] = o[8];
         st->tile_start[E] = at;
@@ -725,7 +731,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
 
   const uint32_t tmem = st->tmem_base;
-  const int total = st->total_tiles;
+  const int total = st->total_tiles, workers = st->workers;
   volatile int* abort = &st->abort;
   auto slot_of = [&](int row) { return sorts ? st->perm[row] : __ldg(p.perm + row); };
   auto tile_of = [&](int t) { return decode_tile(st->tile_start, st->off, E, n_tiles, C::TILE_M, t); };
@@ -1282,12 +1288,7 @@ cudaError_t launch_epi(const AMaps& a, const CUtensorMap& b, Params p, cudaStrea
   if (p.split > 1)
     return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(static_cast<unsigned>(bound * p.split)), dim3(THREADS),
                     smem_bytes<MODE>(), s, false, p.split, a, b, p);
-  // With at most one row block per expert on average (weight streaming), size
-  // the grid so that every CTA takes the same number of tiles.
-  long long tiles = bound;
-  if (p.M <= static_cast<long long>(tile_m) * p.E) tiles = (p.M < p.E ? p.M : p.E) * n_tiles;
-  const long long waves = (tiles + workers - 1) / workers;
-  const int grid = static_cast<int>((tiles + waves - 1) / waves);
+  const int grid = static_cast<int>(bound < workers ? bound : workers);
   return launch_k(gemm_fp8_kernel<EPI, MODE>, dim3(grid), dim3(THREADS), smem_bytes<MODE>(), s, false, 1, a,
                   b, p);
 }
