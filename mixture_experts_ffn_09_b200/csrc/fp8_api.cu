@@ -41,8 +41,8 @@ __global__ void __launch_bounds__(256) count_selected_kernel(const int64_t* __re
 // slot's row (stable, by slot).  Slots are taken 1024 at a time in order; a
 // slot's rank is that within its warp (match), behind the earlier warps'
 // counts and the earlier slots' rows.  One launch instead of three (counts,
-// scan, scatter) for batches that the gate_up GEMM does not sort itself: 512
-// slots of 64 experts 4 us instead of 12.
+// scan, scatter) for batches that the gate_up GEMM does not sort itself: 12 -> 4
+// us, measured with 192 slots of 64 experts.
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallSlots = 4096;
 

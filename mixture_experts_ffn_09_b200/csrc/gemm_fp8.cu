@@ -19,12 +19,16 @@
 //   kPair  256 rows x 256 on two CTAs: half the weight bytes per CTA;
 //   kFew   32 rows x 256, for weight streaming: the MMAs are as tall as
 //          kOne's, but only 32 rows of A are loaded (by token, with gather4,
-//          where the rows are not sorted yet), one warp per half reads them,
-//          and where tiles are few a cluster shares out a tile's blocks and
-//          adds its sums over distributed shared memory.
-// 8192 rows of 4096 x 14336 (kPair): 445 us, 2.16 PFLOP/s.  9973 rows over 64
-// experts of 1408 x 2048, unevenly (kOne): 60 us.  16 rows of 4096 x 14336
-// (kFew): 20 us, the weights at 2.9 TB/s.
+//          where the rows are not sorted yet), and where tiles are few a
+//          cluster shares out a tile's blocks and adds its sums over
+//          distributed shared memory.  The second half's rows are made
+//          accumulator rows 32..63 (its A operand starts 32 rows early), so
+//          that four warps read a block, a half and a weight block each, and
+//          no longer take longer than its MMAs (16 rows of 4096 x 14336: 20.7
+//          -> 18.7 us).
+// 8192 rows of 4096 x 14336 (kPair): 440 us, 2.19 PFLOP/s, at the board's power
+// limit (1.4 to 1.5 GHz).  9973 rows over 64 experts of 1408 x 2048, unevenly
+// (kOne): 60 us.  16 rows of 4096 x 14336 (kFew): 19 us, the weights at 3.1 TB/s.
 //
 // One persistent CTA per SM (or pair of CTAs per two SMs), 384 threads:
 //   warp 0      TMA producer: A rows x 128 columns and B rows (256, or this CTA's
@@ -40,8 +44,8 @@
 //               conflict-free access;
 //   warps 4..11 epilogue: four warps per half, 32 TMEM lanes (rows) each, all
 //               128 columns of the half: 128 fp32 sums per thread.  In kFew
-//               only the two warps of lanes 0..31 have rows; all eight finish
-//               them.
+//               the warps of lanes 0..63 read, 64 sums per thread, and all
+//               eight finish the rows.
 // Registers move from warps 0..3 (72 each) to the epilogue (216): 128 * 72 +
 // 256 * 216 of the launch's 384 * 168.
 //
