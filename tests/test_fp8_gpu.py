@@ -69,7 +69,9 @@ def check_norm(x, r, w, eps, o):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,D", [(1, 1), (3, 7), (1, 128), (5, 130), (33, 264), (2, 4096), (7, 2567),
                                  (1000, 96), (3, 8192), (2, 8200), (2, 16376), (3, 16384), (2, 32768),
-                                 (2, 8193), (2, 16383), (2, 32761)])
+                                 (2, 8193), (2, 16383), (2, 32761),
+                                 (400, 5), (400, 130), (400, 259), (400, 516), (400, 1020), (400, 1032), (400, 2567),
+                                 (300, 16383), (300, 32761), (300, 32768)])      # more rows than SMs take at once
 def test_norm(dtype, T, D):
     x, r = randn(T, D, seed=1).to(dtype), randn(T, D, seed=2, std=3.0).to(dtype)
     w = (1 + 0.3 * randn(D, seed=3)).to(dtype)
@@ -375,7 +377,7 @@ def test_experts(T, D, F, E, K):
 
 @pytest.mark.parametrize("T,D,F,E,K", [(1, 2048, 1152, 2, 1), (3, 2064, 1040, 4, 2),     # K blocks over a cluster
                                        (600, 256, 400, 8, 2), (2100, 128, 144, 8, 2),      # 128-row tiles
-                                       (64, 144, 144, 64, 6), (77, 128, 144, 64, 5), (48, 128, 128, 256, 8),   # 384, 385 slots
+                                       (2, 128, 144, 256, 192), (64, 144, 144, 64, 6), (77, 128, 144, 64, 5), (48, 128, 128, 256, 8),   # 384, 385 slots
                                        (1700, 256, 272, 4, 2), (4700, 144, 144, 2, 1)])    # pairs of CTAs
 def test_experts_row_forms(T, D, F, E, K):
     args = make_experts(T, D, F, E, K, seed=40)
@@ -590,3 +592,73 @@ def test_block_captured_twice():
     graphs[0].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], blk(xs[0], xs[0]))
+
+
+# ----------------------------------------------------- beyond the small cases
+def test_product_offsets_at_four_bytes():
+    a, sa = rows8(90, 272, 1)
+    w, sw = weight8(3, 72, 272, 2)
+    out, want = torch.zeros(90, 72, device="cuda"), torch.zeros(90, 72, device="cuda")
+    o = torch.tensor([7, 0, 30, 41, 90], dtype=torch.int32, device="cuda")
+    moe.gemm_fp8(a, sa, w, sw, out, offsets=o[1:])
+    moe.gemm_fp8(a, sa, w, sw, want, offsets=o[1:].clone())
+    assert torch.equal(out, want) and bool(out.abs().sum() > 0)
+
+
+def test_debug_sync_gives_the_same():
+    args = make_experts(40, 256, 384, 8, 2, seed=3)
+    want = run_experts(args)
+    before = moe.set_debug_sync(5000)
+    try:
+        assert torch.equal(run_experts(args), want)
+    finally:
+        moe.set_debug_sync(before)
+
+
+def test_norm_past_32_bits():
+    T, D = 270_000, 8192                          # 2.2e9 elements
+    x = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(1))
+    w = (1 + 0.3 * randn(D, seed=3)).bfloat16()
+    o = run_norm(x, None, w, 1e-6, sum_out=False)
+    check_norm(x[-3:], None, w, 1e-6, {k: v if v is None else v[-3:] for k, v in o.items()})
+
+
+def test_select_past_32_bits():
+    T, E = 8_400_000, 256                         # 2.15e9 logits
+    lg = torch.empty(T, E, device="cuda").normal_(generator=gen(1))
+    sel, w = torch.empty(T, 8, dtype=torch.int64, device="cuda"), torch.empty(T, 8, device="cuda")
+    moe.select_experts(lg, 8, True, sel, w, score="sigmoid", groups=8, top_groups=4, group_score="top2")
+    for part in (slice(0, 2000), slice(T - 2000, T)):
+        want, w64 = R.select(lg[part], 8, True, score="sigmoid", groups=8, top_groups=4, group_score="top2")
+        assert torch.equal(sel[part], want)
+        assert ((w[part].double() - w64).abs() <= 1e-6).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(70_000, 32_768, 128), (280_000, 64, 8192)])      # out, or a, passes 2^31 bytes
+def test_product_past_32_bits(M, N, K):
+    a = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(std=150, generator=gen(1)).clamp_(-448, 448).to(F8)
+    sa = torch.rand(M, R.nblk(K), generator=gen(2), device="cuda") / 150
+    w, sw = weight8(1, N, K, 3)
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    moe.gemm_fp8(a, sa, w, sw, out)
+    for part in (slice(0, 40), slice(M - 40, M)):
+        C, S, _ = R.product(a[part], sa[part], w, sw, [0, 40])
+        gamma = (128 + R.nblk(K) + 4) * 2 * U32       # as in check_product
+        assert ((out[part].double() - C).abs() <= S * gamma + C.abs() * HALF[torch.bfloat16] * 1.01).all()
+
+
+def test_experts_past_32_bits():
+    """The intermediate and the experts' outputs pass 2^31 elements; first and last tokens against a call of their own."""
+    T, D, F, E, K = 34_000, 8192, 8192, 8, 8
+    args = make_experts(64, D, F, E, K, seed=9)
+    big = [v.repeat((T // 64 + 1,) + (1,) * (v.dim() - 1))[:T].contiguous() if i < 4 else v for i, v in enumerate(
+        [args[0].view(torch.uint8), *args[1:]])]
+    big[0] = big[0].view(F8)
+    out, few = run_experts(big), run_experts(args)
+    for t in range(0, T, 64):
+        n = min(64, T - t)
+        if t and t + 128 < T:
+            continue
+        # the same values, added in another order and rounded to fp16 blocks and bf16
+        d = (out[t:t + n].double() - few[:n].double()).abs()
+        assert (d <= few[:n].double().abs() * 2.0 ** -7 + few[:n].double().abs().amax(1, keepdim=True) * 2.0 ** -9).all()
