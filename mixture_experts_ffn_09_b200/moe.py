@@ -22,6 +22,7 @@ top of these calls; :class:`MoEBlockFP8` is the block in 8 bits.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -191,9 +192,9 @@ def _dtype_code(t) -> int:
     import torch
     if t.dtype is torch.float32:
         return F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return BF16
-    if t.dtype == torch.float64:
+    if t.dtype is torch.float64:
         return F64
     return -1
 
@@ -413,8 +414,8 @@ def _blocks(n: int) -> int:
     return -(-n // QUANT_BLOCK)
 
 
-def _rows(t) -> int:
-    return t.numel() // t.shape[-1] if t.shape[-1] else 0
+def _rows(shape) -> int:
+    return math.prod(shape[:-1]) if len(shape) != 2 else shape[0]
 
 
 # The 8-bit calls take microseconds on the GPU at decode sizes, so their
@@ -429,7 +430,7 @@ def _fast():
     if _torch is None:
         import torch
         _torch = torch
-    return _torch, _lib or lib(), _torch.cuda.current_device() if _torch.cuda.is_initialized() else -1
+    return _torch, _lib or lib(), _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -1
 
 
 def _raw_stream(stream, dev: int):
@@ -445,17 +446,17 @@ def _want(t, shape, dtype, name, dev, required=True):
         if required:
             raise ValueError(f"{name} is required")
         return 0
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev >= 0:
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev or dev < 0:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
 
 
 def add_rmsnorm(x, weight, eps: float, residual=None, sum_out=None, out=None, out8=None,
@@ -466,7 +467,7 @@ def add_rmsnorm(x, weight, eps: float, residual=None, sum_out=None, out=None, ou
     torch, L, dev = _fast()
     shape, dtype = x.shape, x.dtype
     D = shape[-1]
-    T = _rows(x)
+    T = _rows(x.shape)
     dt = _dtype_code(x)
     ok = dt in (F32, BF16) and T > 0       # else the library says what is wrong
     px, pw, pr, ps, po, p8, pc = (
@@ -512,7 +513,7 @@ def select_experts(logits, K: int, norm_topk_prob: bool, selected_experts, routi
     selected_experts int64 and routing_weights float32 of K per row."""
     torch, L, dev = _fast()
     E = logits.shape[-1]
-    T = _rows(logits)
+    T = _rows(logits.shape)
     pl = ps = pw = None
     if T > 0 and K >= 1:
         pl = _want(logits, logits.shape, torch.float32, "logits", dev)
@@ -531,7 +532,7 @@ def route_groups(x, router, K: int, norm_topk_prob: bool, router_logits, selecte
     :func:`select_experts`; router_logits (T, E) float32 is written."""
     torch, L, dev = _fast()
     D = x.shape[-1]
-    T = _rows(x)
+    T = _rows(x.shape)
     E = router.shape[0]
     dt = _dtype_code(x)
     px = pr = pb = pl = ps = pw = None
@@ -585,7 +586,7 @@ def experts_forward_fp8(x, x_scales, selected_experts, routing_weights, gate_up_
     (T, K) int64, routing_weights (T, K) float32; out bfloat16 like x."""
     torch, L, dev = _fast()
     D = x.shape[-1]
-    T = _rows(x)
+    T = _rows(x.shape)
     E, F = down_proj.shape[0], down_proj.shape[-1]
     K = selected_experts.shape[-1]
     ptrs, ws_bytes, pws = (None,) * 9, 0, None
@@ -823,7 +824,7 @@ class MoEBlockFP8:
             with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
                 return self.forward(x, residual)
         E, F, D = int(self.down_proj.shape[0]), int(self.down_proj.shape[-1]), int(x.shape[-1])
-        T, K = _rows(x), self.top_k
+        T, K = _rows(x.shape), self.top_k
         new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
         x8, xs = new(x.shape, torch.float8_e4m3fn), new((T, _blocks(D)), torch.float32)
         if self.norm_weight is not None:
