@@ -42,7 +42,9 @@ __global__ void __launch_bounds__(256) count_selected_kernel(const int64_t* __re
 // slot's rank is that within its warp (match), behind the earlier warps'
 // counts and the earlier slots' rows.  One launch instead of three (counts,
 // scan, scatter) for batches that the gate_up GEMM does not sort itself: 12 -> 4
-// us, measured with 192 slots of 64 experts.
+// us, measured with 192 slots of 64 experts.  A whole call against the other path:
+// 64 experts, 2040 slots 33 | 35 us, 3072 35.4 | 35.8, 4080 39.6 | 37.5; 256
+// experts, 4096 slots 54 | 66.
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallSlots = 4096;
 

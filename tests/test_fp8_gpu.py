@@ -377,7 +377,7 @@ def test_experts(T, D, F, E, K):
 
 @pytest.mark.parametrize("T,D,F,E,K", [(1, 2048, 1152, 2, 1), (3, 2064, 1040, 4, 2),     # K blocks over a cluster
                                        (600, 256, 400, 8, 2), (2100, 128, 144, 8, 2),      # 128-row tiles
-                                       (2, 128, 144, 256, 192), (64, 144, 144, 64, 6), (77, 128, 144, 64, 5), (48, 128, 128, 256, 8),   # 384, 385 slots
+                                       (2, 128, 144, 256, 192), (600, 128, 144, 64, 6), (512, 128, 144, 256, 8), (64, 144, 144, 64, 6), (77, 128, 144, 64, 5), (48, 128, 128, 256, 8),   # 384, 385 slots
                                        (1700, 256, 272, 4, 2), (4700, 144, 144, 2, 1)])    # pairs of CTAs
 def test_experts_row_forms(T, D, F, E, K):
     args = make_experts(T, D, F, E, K, seed=40)
