@@ -389,9 +389,17 @@ __global__ void __launch_bounds__(kWarps * 32) select_experts_kernel(const Selec
     const int run = 32 / a.groups;
     float m1 = key_value(key[0]), m2 = EPL > 1 ? key_value(key[1]) : -INFINITY;
     if (top2 && !a.bias) {
-      // the scores of the two largest logits, read again without truncation
-      m1 = score(clean(__ldg(lrow + lane * EPL + 7 - static_cast<int>(key[0] & 7u))));
-      if (EPL > 1) m2 = score(clean(__ldg(lrow + lane * EPL + 7 - static_cast<int>(key[1] & 7u))));
+      // Scores of logits: the two largest of l itself.  A truncated logit is off
+      // by up to |l| 2^-20, whatever its score, and of more than two logits that
+      // agree but for the truncated bits the list's head need not hold the largest.
+      float l1 = -INFINITY, l2 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        l2 = fmaxf(l2, fminf(l1, l[i]));
+        l1 = fmaxf(l1, l[i]);
+      }
+      m1 = score(l1);
+      if (EPL > 1) m2 = score(l2);
     }
     for (int o = 1; o < run; o <<= 1) {
       const float o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);

@@ -204,6 +204,24 @@ def test_select_masked_and_not_finite(o, bias):
     check_select(l, 6, False, selection_bias=b, **o)
 
 
+@pytest.mark.parametrize("E,groups", [(256, 8), (64, 8), (250, 10)])       # groups as runs of lanes, and any size
+@pytest.mark.parametrize("offset", [0.0, 100.0, 1000.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_select_group_candidates_few_ulps_apart(E, groups, offset, score):
+    """The two best of a group among several that differ in their last bits, far from zero."""
+    T, size = 400, E // groups
+    ulp = 2.0 ** -14 if offset else 2.0 ** -23
+    l = offset - 100.0 + torch.zeros(T, groups, size, device="cuda")
+    n = min(size, 6)
+    near = torch.randint(0, 16, (T, groups, n), generator=gen(1), device="cuda") * ulp
+    l[:, :, :n] = offset + near.to(torch.float32)
+    l[0] = offset - 100.0
+    l[0, 0, :3] = torch.tensor([offset, offset, offset + 7 * ulp], device="cuda")
+    l[0, 1, :2] = torch.tensor([offset + 0.01, offset - 0.0099], device="cuda")
+    for top in (1, groups // 2):
+        check_select(l.view(T, E), 2, False, score=score, groups=groups, top_groups=top, group_score="top2")
+
+
 def test_route_groups():
     """Both dtypes: the logits are the router's, the choice is that of select_experts on them."""
     for dtype, T, D, E in ((torch.bfloat16, 300, 264, 64), (torch.float32, 37, 33, 20)):
