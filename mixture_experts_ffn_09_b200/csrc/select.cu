@@ -44,6 +44,7 @@ __device__ __forceinline__ unsigned int order_key(float v) {
 
 struct Shared {
   float by[kWarps][kMaxExperts];        // what groups are ranked by
+  float least[kWarps][kMaxExperts], most[kWarps][kMaxExperts];   // bounds of a group's score
   unsigned char keep[kWarps][kMaxExperts];   // group stays
   int sel[kWarps][kMaxExperts + 1];
   float val[kWarps][kMaxExperts + 1];   // group scores, then the ranks of the chosen
@@ -65,6 +66,22 @@ __device__ __forceinline__ float score_tol(int score) { return score == 0 ? 3.81
 // and a + tol may be off for other reasons.
 __device__ __forceinline__ bool surely_above(float a, float b, float tol) {
   return a - b > tol + 1.2e-6f * (fabsf(a) + fabsf(b));
+}
+
+// What a group's score v, the sum of its two largest c (pair) or the largest,
+// may be for sure: its error is that of c relative to each of the two, as in
+// surely_above, and does not shrink where they cancel.  An overflow says
+// nothing; a -inf among the two (m2 <= m1) is one in 64 bits as well.
+__device__ __forceinline__ float group_slack(float m1, float m2, bool pair) {
+  return 1.2e-6f * (pair ? fabsf(m1) + fabsf(m2) : fabsf(m1));
+}
+__device__ __forceinline__ float group_least(float m1, float m2, bool pair) {
+  const float slack = group_slack(m1, m2, pair);
+  return slack <= FLT_MAX ? (pair ? m1 + m2 : m1) - slack : -INFINITY;
+}
+__device__ __forceinline__ float group_most(float m1, float m2, bool pair) {
+  const float slack = group_slack(m1, m2, pair);
+  return slack <= FLT_MAX ? (pair ? m1 + m2 : m1) + slack : (pair ? m2 : m1) == -INFINITY ? -INFINITY : INFINITY;
 }
 
 // A lane's i-th rank as a sortable key: the rank without its lowest three
@@ -299,6 +316,7 @@ __global__ void __launch_bounds__(kWarps * 32) select_experts_kernel(const Selec
   };
   const bool top2 = a.group_score == 1;
   const int size = E / a.groups;
+  const bool pair = top2 && size > 1;            // a group's score is a sum
   const bool whole = E == 32 * EPL && a.groups <= 32 && 32 % a.groups == 0;   // groups are runs of lanes
   const float tol = score_tol(a.score);
   bool sure = true;
@@ -356,10 +374,12 @@ __global__ void __launch_bounds__(kWarps * 32) select_experts_kernel(const Selec
         m2 = fmaxf(m2, fminf(m1, v));
         m1 = fmaxf(m1, v);
       }
-      sh.val[warp][g] = top2 && size > 1 ? m1 + m2 : m1;
+      sh.val[warp][g] = pair ? m1 + m2 : m1;
+      sh.least[warp][g] = group_least(m1, m2, pair);
+      sh.most[warp][g] = group_most(m1, m2, pair);
     }
     __syncwarp();
-    float worst = INFINITY, next = -INFINITY;
+    float worst = INFINITY, next = -INFINITY;    // of the kept, the least; of the others, the most
     for (int g = lane; g < a.groups; g += 32) {
       const float v = sh.val[warp][g];
       int ahead = 0;
@@ -369,10 +389,10 @@ __global__ void __launch_bounds__(kWarps * 32) select_experts_kernel(const Selec
       }
       const bool keep = ahead < a.top_groups;
       sh.keep[warp][g] = keep;
-      if (keep) worst = fminf(worst, v); else next = fmaxf(next, v);
+      if (keep) worst = fminf(worst, sh.least[warp][g]); else next = fmaxf(next, sh.most[warp][g]);
     }
     if ((a.bias || top2) && a.top_groups < a.groups)       // the largest logit is exact here
-      sure = surely_above(-warp_max(-worst), warp_max(next), 2.f * tol);
+      sure = -warp_max(-worst) - warp_max(next) > 2.f * tol;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -406,7 +426,7 @@ __global__ void __launch_bounds__(kWarps * 32) select_experts_kernel(const Selec
       m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
       m1 = fmaxf(m1, o1);
     }
-    const float v = top2 && size > 1 ? m1 + m2 : m1;
+    const float v = pair ? m1 + m2 : m1;
     const int g = lane / run;
     int ahead = 0;
     for (int h = 0; h < a.groups; ++h) {
@@ -415,8 +435,9 @@ __global__ void __launch_bounds__(kWarps * 32) select_experts_kernel(const Selec
     }
     const bool keep = ahead < a.top_groups;
     if (a.top_groups < a.groups)
-      sure = surely_above(-warp_max(keep ? -v : -INFINITY), warp_max(keep ? -INFINITY : v),
-                          a.bias || top2 ? 2.f * tol : 0.f);
+      sure = -warp_max(keep ? -group_least(m1, m2, pair) : -INFINITY) -
+                 warp_max(keep ? -INFINITY : group_most(m1, m2, pair)) >
+             (a.bias || top2 ? 2.f * tol : 0.f);
     if (!keep) key[0] = 0u;                      // (the rest of the list is not reached)
   }
 

@@ -222,6 +222,36 @@ def test_select_group_candidates_few_ulps_apart(E, groups, offset, score):
         check_select(l.view(T, E), 2, False, score=score, groups=groups, top_groups=top, group_score="top2")
 
 
+@pytest.mark.parametrize("E,groups", [(64, 32), (60, 30), (256, 8), (250, 10)])       # groups as runs of lanes, and any size
+@pytest.mark.parametrize("size", [1.0, 10.0, 100.0, 1000.0, 1e38])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_select_group_sums_that_cancel(E, groups, size, score):
+    """Biases of opposite signs whose sums lie near each other: a sum's error is that of its terms."""
+    n = E // groups
+    for seed in range(30):
+        b = torch.full((groups, n), -4.0 * min(size, 5e37), device="cuda")
+        b[:, 0] = size * (1 + 0.05 * torch.rand(groups, generator=gen(seed), device="cuda"))
+        b[:, 1] = torch.randint(0, 8, (groups,), generator=gen(seed + 50), device="cuda") * 2e-7 * size - b[:, 0]
+        l = randn(200, E, seed=seed, std=1e-6)
+        check_select(l, 2, False, score=score, selection_bias=b.view(-1), groups=groups, top_groups=1 + seed % (groups - 1),
+                     group_score="top2")
+
+
+def test_select_group_sums_that_cancel_by_truncation():
+    """All scores 1: 5 + 15 u - 5 is more than 5 + 21 u - 5 - 7 u, u = 2^-21."""
+    u = 2.0 ** -21
+    b = torch.full((64,), -20.0, device="cuda")
+    b[:2] = torch.tensor([4 + 15 * u, -6.0])
+    b[8:10] = torch.tensor([4 + 21 * u, -6.0 - 7 * u])
+    l = torch.full((3, 64), 100.0, device="cuda")
+    check_select(l, 2, False, score="sigmoid", selection_bias=b, groups=8, top_groups=1, group_score="top2")
+    b2 = torch.zeros(4, device="cuda")
+    b2[:] = torch.tensor([100.536850, -99.380936, 100.033401, -98.877495])
+    b2 = torch.cat([b2, torch.full((60,), -300.0, device="cuda")])
+    check_select(torch.zeros(3, 64, device="cuda"), 2, False, score="sigmoid", selection_bias=b2, groups=32, top_groups=1,
+                 group_score="top2")
+
+
 def test_route_groups():
     """Both dtypes: the logits are the router's, the choice is that of select_experts on them."""
     for dtype, T, D, E in ((torch.bfloat16, 300, 264, 64), (torch.float32, 37, 33, 20)):
