@@ -252,6 +252,29 @@ def test_select_group_sums_that_cancel_by_truncation():
                  group_score="top2")
 
 
+@pytest.mark.parametrize("E,groups", [(256, 8), (250, 10), (64, 32)])
+@pytest.mark.parametrize("o", [dict(), dict(group_score="top2"), dict(score="sigmoid", group_score="top2")], ids=str)
+@pytest.mark.parametrize("by_bias", [False, True])
+def test_select_whole_groups_masked(E, groups, o, by_bias):
+    """Groups of which nothing, one expert or two are left, kept and dropped; sums that pass fp32's range."""
+    n = E // groups
+    off = torch.zeros(groups, n, dtype=torch.bool, device="cuda")
+    off[: groups // 2] = True
+    off[0, 0] = off[1, : min(n, 2)] = False
+    for extreme in (False, True):
+        l, b = randn(90, E, seed=E), 0.1 * randn(E, seed=3)
+        if by_bias:
+            b[off.view(-1)] = -INF
+            if extreme:
+                b.view(groups, n)[1::3] = -3e38
+                b.view(groups, n)[2::3] = 3e38
+        else:
+            l[:, off.view(-1)] = -INF
+            b = None
+        for top in (1, groups // 2, groups // 2 + 1, groups - 1):
+            check_select(l, min(8, top * n), True, selection_bias=b, groups=groups, top_groups=top, **o)
+
+
 def test_route_groups():
     """Both dtypes: the logits are the router's, the choice is that of select_experts on them."""
     for dtype, T, D, E in ((torch.bfloat16, 300, 264, 64), (torch.float32, 37, 33, 20)):
