@@ -786,9 +786,11 @@ class MoEBlockFP8:
     those of :func:`select_experts`.  Keeps ``router_logits_``,
     ``selected_experts_`` and ``routing_weights_`` of the last call.
 
-    Calls may overlap on several streams: every call takes its buffers, the
-    workspace too, from the allocator's pool of its stream (of the graph,
-    while one is captured), and none is kept for the next call."""
+    Calls may overlap on several streams and in several threads: every call
+    takes its buffers, the workspace too, from the allocator's pool of its
+    stream (of the graph, while one is captured), and none is kept for the next
+    call.  The attributes are set as a call returns, so with several threads
+    they are those of any of them."""
 
     def __init__(self, router, gate_up_proj, down_proj, top_k: int = 2, norm_topk_prob: bool = True,
                  norm_weight=None, eps: float = 1e-6, router_bias=None, **routing):
@@ -827,23 +829,26 @@ class MoEBlockFP8:
         T, K = _rows(x.shape), self.top_k
         new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
         x8, xs = new(x.shape, torch.float8_e4m3fn), new((T, _blocks(D)), torch.float32)
+        total = x if self.norm_weight is not None else None
         if self.norm_weight is not None:
-            self.residual_ = torch.empty_like(x) if residual is not None else x
+            if residual is not None:
+                total = torch.empty_like(x)
             y = torch.empty_like(x)
-            add_rmsnorm(x, self.norm_weight, self.eps, residual,
-                        self.residual_ if residual is not None else None, y, x8, xs)
+            add_rmsnorm(x, self.norm_weight, self.eps, residual, total if residual is not None else None, y, x8, xs)
             x = y
         else:
             quantize_fp8(x.view(T, D), x8.view(T, D), xs, 1)
-        self.router_logits_ = new((T, E), torch.float32)
-        self.selected_experts_ = new((T, K), torch.int64)
-        self.routing_weights_ = new((T, K), torch.float32)
-        route_groups(x, self.router, K, self.norm_topk_prob, self.router_logits_,
-                     self.selected_experts_, self.routing_weights_, self.router_bias, **self.routing)
+        logits, selected = new((T, E), torch.float32), new((T, K), torch.int64)
+        weights = new((T, K), torch.float32)
+        route_groups(x, self.router, K, self.norm_topk_prob, logits, selected, weights, self.router_bias,
+                     **self.routing)
         ws = new(max(experts_workspace_size_fp8(T, D, F, E, K), 1), torch.uint8)
         out = new(x.shape, torch.bfloat16)
-        experts_forward_fp8(x8, xs, self.selected_experts_, self.routing_weights_, self.gate_up_proj,
-                            self.gate_up_scales, self.down_proj, self.down_scales, out, ws)
+        experts_forward_fp8(x8, xs, selected, weights, self.gate_up_proj, self.gate_up_scales, self.down_proj,
+                            self.down_scales, out, ws)
+        # only now: another thread may be inside a call of its own
+        self.residual_, self.router_logits_ = total, logits
+        self.selected_experts_, self.routing_weights_ = selected, weights
         return out
 
     __call__ = forward

@@ -1,4 +1,6 @@
 """The 8-bit path on the GPU against float64 (tests/fp8_lib.py)."""
+import threading
+
 import pytest
 import torch
 
@@ -637,6 +639,29 @@ def test_block_on_streams_at_once():
         got = [blk(x, x, stream=st if i else st.cuda_stream) for i, (x, st) in enumerate(zip(xs, s))]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_block_in_two_threads():
+    """One block, two threads with a stream and tokens of their own, as many of them in each."""
+    blk = make_block()
+    xs = [randn(60, 256, seed=s).bfloat16() for s in (1, 2)]
+    want = [blk(x, x) for x in xs]
+    torch.cuda.synchronize()
+    bad = [None, None]
+
+    def calls(i):
+        st = torch.cuda.Stream()
+        wrong = 0
+        for _ in range(100):
+            wrong += not torch.equal(blk(xs[i], xs[i], stream=st), want[i])
+        bad[i] = wrong
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert bad == [0, 0]
 
 
 def test_block_captured_twice():
