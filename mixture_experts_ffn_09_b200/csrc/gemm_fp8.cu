@@ -324,15 +324,15 @@ __device__ __forceinline__ void umma_fp8(uint32_t d_tmem, uint64_t adesc, uint64
         : "memory");
 }
 
-// Arrives once on `bar` (of both CTAs of a pair) when the MMAs that this
-// thread has issued are complete.
+// Arrives once on `bar` (of a pair in the CTAs of the mask) when the MMAs that
+// this thread has issued are complete.
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint64_t* bar, uint16_t ctas = 3) {
   if constexpr (PAIR)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(ctas)
         : "memory");
   else
     umma_commit(bar);
@@ -863,8 +863,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      // all MMAs issued by this thread complete before TMEM / smem go away
-      commit<PAIR>(&st->mma_done[half]);
+      // All MMAs issued by this thread complete before TMEM / smem go away.  Of a
+      // pair the leader alone is told: only it waits, and an arrival that the peer
+      // does not wait for could reach it after it has left.
+      commit<PAIR>(&st->mma_done[half], 1);
       drain_wait(&st->mma_done[half], 0, p.err, SITE_FP8_MMA);
     }
   } else if (warp == 3) {

@@ -377,6 +377,21 @@ def test_products_at_once():
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
+def test_pair_products_back_to_back():
+    """CTA pairs of one short tile, launched without a pause: each ends with nothing of its own still on the way."""
+    a, sa = rows8(800, 16, 1)
+    w, sw = weight8(1, 2048, 16, 2)
+    want = torch.empty(800, 2048, device="cuda")
+    moe.gemm_fp8(a, sa, w, sw, want)
+    C, S, _ = R.product(a, sa, w, sw, [0, 800])
+    assert ((want.double() - C).abs() <= S * 133 * 2 * U32 + C.abs() * U32 * 1.01).all()       # as in check_product
+    outs = [torch.empty_like(want) for _ in range(4)]
+    for i in range(400):
+        moe.gemm_fp8(a, sa, w, sw, outs[i % 4])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def test_product_offsets_out_of_order_are_clamped():
     """Offsets beyond M count as M, descending ones as the one before."""
     a, sa = rows8(40, 128, 1)
