@@ -284,13 +284,13 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, 
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives once on the barrier at this offset in both CTAs of the pair when
-// the pair's MMAs issued so far have completed.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+// Arrives once on the barrier at this offset in the CTAs of the mask (both of
+// the pair) when the pair's MMAs issued so far have completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t ctas = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(ctas)
       : "memory");
 }
 
@@ -591,7 +591,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         umma_commit_pair(&st->tfull[acc]);
       }
-      umma_commit_pair(&st->mma_done);
+      // on the leader alone: only it waits, and an arrival that the peer does
+      // not wait for could reach it after it has left
+      umma_commit_pair(&st->mma_done, 1);
       int dummy = 0;
       mbar_wait(&st->mma_done, 0, &dummy, p.err, SITE_PAIR_MMA);
     }
