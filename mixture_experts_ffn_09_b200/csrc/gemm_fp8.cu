@@ -125,7 +125,7 @@ __device__ __forceinline__ bool mbar_try_loop(uint32_t bar, uint32_t parity) {
 }
 
 // The same for a whole (converged) warp: lane 0 tries, a vote makes the result
-// uniform.
+// uniform (and no more than that: see warp_wait).
 __device__ __forceinline__ bool mbar_try_loop_warp(uint32_t bar, uint32_t parity, int lane) {
   uint32_t ok;
   asm volatile(
@@ -462,10 +462,15 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   if (__builtin_expect(mbar_try_loop(smem_u32(bar), parity), 1)) return true;
   return mbar_wait(bar, parity, abort, err, site);
 }
-// The same for a converged warp, with the same result in every lane.
+// The same for a converged warp, with the same result in every lane.  The vote
+// tells the lanes what lane 0 has seen but orders no memory; __syncwarp makes
+// what the barrier hands over theirs too.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, volatile int* abort,
                                           unsigned int* err, unsigned int site) {
-  if (__builtin_expect(mbar_try_loop_warp(smem_u32(bar), parity, lane), 1)) return true;
+  if (__builtin_expect(mbar_try_loop_warp(smem_u32(bar), parity, lane), 1)) {
+    __syncwarp();
+    return true;
+  }
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, site));
 }
 
