@@ -472,7 +472,8 @@ MOE_API int moe_set_fused_gather(int mode);
  * dependent launch (OFF by default): each kernel's set-up (barriers, tensor
  * memory, descriptor prefetch) then overlaps the end of the previous kernel,
  * and it waits for that kernel before reading or writing shared buffers.
- * Same results either way; it saves 0-2% of a forward.  Off by default
+ * Same results either way; it saves 0-2% of a forward.  The 8-bit calls do
+ * not use it.  Off by default
  * because, with it on, back-to-back forwards of the 64-expert fine-grained
  * layer were seen to stall on B200 (no cause found; none with it off).
  * Returns the previous setting.

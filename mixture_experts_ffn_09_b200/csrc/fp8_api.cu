@@ -356,7 +356,7 @@ moe_status_t moe_route_groups(const void* x, const void* router, const float* ro
   unsigned int* err = nullptr;
   if ((st = device_ready(&err)) != MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // the router kernel writes its logits and nothing else
+  // the router kernel writes its logits and nothing else (no dependent launch)
   RouteArgs r{};
   r.x = x;
   r.router = router;
@@ -459,6 +459,7 @@ moe_status_t moe_experts_forward_fp8(const void* x_fp8, const float* x_scales,
   const int Ti = static_cast<int>(T), Di = static_cast<int>(D), Fi = static_cast<int>(F);
   const int R = Ti * K;
 
+  // no programmatic dependent launch here, whatever moe_set_pdl says
   StageScope scope(s);
   scope.begin();
   const bool sorts = gemm_fp8_sorts(R, L.gather);     // in the gate_up GEMM
@@ -472,16 +473,16 @@ moe_status_t moe_experts_forward_fp8(const void* x_fp8, const float* x_scales,
     if (st != MOE_OK) return st;
     const bool own_scan = static_cast<long long>(L.B) * E <= kScatterScansItself;
     if (!own_scan) {
-      st = launched(launch_permute_scan(bcount, L.B, E, bbase, totals, s), s, "permute scan");
+      st = launched(launch_permute_scan(bcount, L.B, E, bbase, totals, false, s), s, "permute scan");
       if (st != MOE_OK) return st;
     }
     st = launched(launch_permute_scatter(idx32, own_scan ? nullptr : bbase, own_scan ? nullptr : totals,
-                                         bcount, Ti, K, E, offsets, perm, pos, nullptr, nullptr, s),
+                                         bcount, Ti, K, E, offsets, perm, pos, nullptr, nullptr, false, s),
                   s, "permute scatter");
     if (st != MOE_OK) return st;
   }
   if (!L.gather) {
-    st = launched(launch_gather_rows(perm, offsets, pos, Ti, E, K, x_fp8, Di, ws + L.xperm, s), s,
+    st = launched(launch_gather_rows(perm, offsets, pos, Ti, E, K, x_fp8, Di, ws + L.xperm, false, s), s,
                   "row gather");
     if (st != MOE_OK) return st;
   }

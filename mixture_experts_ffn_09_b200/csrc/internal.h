@@ -48,6 +48,7 @@ struct RouteArgs {
   float dyn_threshold;      // > 0: drop kept experts whose renormalised share is below it
   uint8_t* slot_kept;       // (T, K): 1 where the slot's expert output enters out
   float* bal_partial;       // (parts, 3, E): per-CTA sums of scores, gate, gate > 0
+  bool pdl;                 // launched with programmatic dependent launch
 };
 
 // Slots the router dropped carry this expert index in idx32 (= E).
@@ -73,8 +74,9 @@ cudaError_t launch_router_tc(const RouteArgs& a, cudaStream_t s);
 
 // Per-expert column scans of the router's 32-token histograms (B, E):
 // blockbase[b, e] = rows of expert e in blocks before b; totals[e].
+// (pdl, here and below: launched with programmatic dependent launch.)
 cudaError_t launch_permute_scan(const int* blockcounts, int B, int E, int* blockbase,
-                                int* totals, cudaStream_t s);
+                                int* totals, bool pdl, cudaStream_t s);
 
 // Block-count tables up to this many entries (blocks x experts) are scanned
 // inside the scatter kernel: each of its blocks reads the whole table.
@@ -89,13 +91,14 @@ constexpr long long kScatterScansItself = 4096;
 cudaError_t launch_permute_scatter(const int* idx32, const int* blockbase, const int* totals,
                                    const int* blockcounts, int T, int K, int E, int* offsets,
                                    int* perm, int* pos, uint8_t* slot_kept, int* sched,
-                                   cudaStream_t s);
+                                   bool pdl, cudaStream_t s);
 
 // x_perm[pos[t, k], :] = x[t, :] for every slot that was given a row
 // (pos >= 0; perm is the inverse map, offsets[E] the live row count): by
 // sorted row while x fits in L2, else by token with each row of x read once.
 cudaError_t launch_gather_rows(const int* perm, const int* offsets, const int* pos, int T, int E,
-                               int K, const void* x, int row_bytes, void* x_perm, cudaStream_t s);
+                               int K, const void* x, int row_bytes, void* x_perm, bool pdl,
+                               cudaStream_t s);
 
 // out[t, :] = sum_k w[t, k] * Y[pos[t, k], :], fp32 sum in k order; slots
 // with pos < 0 (dropped) add nothing.
@@ -239,6 +242,7 @@ class StageScope {             // one forward's stage timing (off unless profili
 };
 
 int num_sms();
+bool pdl_enabled();                      // moe_set_pdl
 unsigned long long kernel_launches();   // accepted launches so far (note_launch)
 
 // One CTA waiting (bounded) on an mbarrier nothing arrives at.

@@ -420,6 +420,7 @@ moe_status_t moe_route_ex(const void* x, const void* router, const float* router
   DevInfo* dev = nullptr;
   if ((st = device_info(&dev)) != MOE_OK) return st;
   moe::RouteArgs a{};
+  a.pdl = moe::pdl_enabled();
   a.x = x;
   a.router = router;
   a.router_bias = router_bias;
@@ -556,6 +557,7 @@ moe_status_t ffn_forward_impl(const void* x, const void* router, const void* gat
   }
   e = timer.run(0, [&] {
     moe::RouteArgs a{};
+    a.pdl = moe::pdl_enabled();
     a.x = x;
     a.router = router;
     a.router_bias = router_bias;
@@ -591,16 +593,18 @@ moe_status_t ffn_forward_impl(const void* x, const void* router, const void* gat
     // a small block-count table is scanned by the scatter blocks themselves
     const bool own_scan = static_cast<long long>(L.B) * E <= moe::kScatterScansItself;
     if (!own_scan) {
-      r = moe::launch_permute_scan(bcount, L.B, E, bbase, totals, s);
+      r = moe::launch_permute_scan(bcount, L.B, E, bbase, totals, moe::pdl_enabled(), s);
       if (r != cudaSuccess) return r;
       if (!debug_wait(dev, s, "permute scan")) return cudaErrorTimeout;
     }
     r = moe::launch_permute_scatter(idx32, own_scan ? nullptr : bbase, own_scan ? nullptr : totals,
-                                    bcount, Ti, K, E, offsets, perm, pos, slot_kept, sched, s);
+                                    bcount, Ti, K, E, offsets, perm, pos, slot_kept, sched,
+                                    moe::pdl_enabled(), s);
     if (r != cudaSuccess) return r;
     if (!debug_wait(dev, s, "permute scatter")) return cudaErrorTimeout;
     if (fused_gather) return r;
-    r = moe::launch_gather_rows(perm, offsets, pos, Ti, E, K, x, Di * elem, xperm, s);
+    r = moe::launch_gather_rows(perm, offsets, pos, Ti, E, K, x, Di * elem, xperm, moe::pdl_enabled(),
+                                s);
     if (r != cudaSuccess) return r;
     return debug_wait(dev, s, "row gather") ? cudaSuccess : cudaErrorTimeout;
   });

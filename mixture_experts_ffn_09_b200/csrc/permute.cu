@@ -267,33 +267,34 @@ __global__ void __launch_bounds__(kGatherThreads) gather_by_token_kernel(
 }  // namespace
 
 cudaError_t launch_permute_scan(const int* blockcounts, int B, int E, int* blockbase, int* totals,
-                                cudaStream_t s) {
-  return launch_k(permute_scan_kernel, dim3(E), dim3(kScanThreads), 0, s, pdl_enabled(), 1,
+                                bool pdl, cudaStream_t s) {
+  return launch_k(permute_scan_kernel, dim3(E), dim3(kScanThreads), 0, s, pdl, 1,
                   blockcounts, B, E, blockbase, totals);
 }
 
 cudaError_t launch_permute_scatter(const int* idx32, const int* blockbase, const int* totals,
                                    const int* blockcounts, int T, int K, int E, int* offsets,
                                    int* perm, int* pos, uint8_t* slot_kept, int* sched,
-                                   cudaStream_t s) {
+                                   bool pdl, cudaStream_t s) {
   const int B = (T + kRouterTokensPerCta - 1) / kRouterTokensPerCta;
-  return launch_k(permute_scatter_kernel, dim3(B), dim3(kScatterThreads), 0, s, pdl_enabled(), 1,
+  return launch_k(permute_scatter_kernel, dim3(B), dim3(kScatterThreads), 0, s, pdl, 1,
                   idx32, blockbase, totals, blockcounts, T, K, E, offsets, perm, pos, slot_kept,
                   sched);
 }
 
 cudaError_t launch_gather_rows(const int* perm, const int* offsets, const int* pos, int T, int E,
-                               int K, const void* x, int row_bytes, void* x_perm, cudaStream_t s) {
+                               int K, const void* x, int row_bytes, void* x_perm, bool pdl,
+                               cudaStream_t s) {
   constexpr size_t kL2ResidentBytes = 48u << 20;   // x read per copy while it stays in L2
   const int warps = kGatherThreads / 32;
   if (static_cast<size_t>(T) * row_bytes <= kL2ResidentBytes) {
     const long long rows = static_cast<long long>(T) * K;
     return launch_k(gather_by_row_kernel, dim3(static_cast<unsigned>((rows + warps - 1) / warps)),
-                    dim3(kGatherThreads), 0, s, pdl_enabled(), 1, perm, offsets, E, K,
+                    dim3(kGatherThreads), 0, s, pdl, 1, perm, offsets, E, K,
                     static_cast<const uint8_t*>(x), row_bytes, static_cast<uint8_t*>(x_perm));
   }
   return launch_k(gather_by_token_kernel, dim3((T + warps - 1) / warps), dim3(kGatherThreads), 0, s,
-                  pdl_enabled(), 1, pos, T, K, static_cast<const uint8_t*>(x), row_bytes,
+                  pdl, 1, pos, T, K, static_cast<const uint8_t*>(x), row_bytes,
                   static_cast<uint8_t*>(x_perm));
 }
 

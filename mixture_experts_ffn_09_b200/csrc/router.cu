@@ -282,7 +282,7 @@ cudaError_t launch_typed(const RouteArgs& a, cudaStream_t s) {
     }
   }
   return launch_k(router_topk_kernel<Tin, kVec>, dim3(blocks), dim3(kWarps * 32), smem, s,
-                  pdl_enabled(), 1, a);
+                  a.pdl, 1, a);
 }
 
 }  // namespace

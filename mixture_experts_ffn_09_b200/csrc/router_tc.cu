@@ -621,7 +621,7 @@ cudaError_t launch_npad(const RouteArgs& a, cudaStream_t s) {
   while (S < 8 && m_tiles * S * 2 <= num_sms() && S * 2 <= p.num_kb && S * 2 <= kMaxSlots) S *= 2;
   p.S = S;
   return launch_k(router_tc_kernel<NPAD>, dim3(m_tiles * p.S), dim3(THREADS), smem_bytes<NPAD>(), s,
-                  pdl_enabled(), p.S, mx, mw, p);
+                  a.pdl, p.S, mx, mw, p);
 }
 
 }  // namespace

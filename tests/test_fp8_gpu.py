@@ -716,6 +716,18 @@ def test_product_offsets_at_four_bytes():
     assert torch.equal(out, want) and bool(out.abs().sum() > 0)
 
 
+@pytest.mark.parametrize("T", [40, 900, 30000])        # slots sorted by gate_up, by one CTA, and over many
+def test_dependent_launch_setting_changes_nothing(T):
+    args = make_experts(T, 128, 144, 8, 2, seed=3)
+    want = run_experts(args)
+    before = moe.set_pdl(True)
+    try:
+        for _ in range(3):
+            assert torch.equal(run_experts(args), want)
+    finally:
+        moe.set_pdl(before)
+
+
 def test_debug_sync_gives_the_same():
     args = make_experts(40, 256, 384, 8, 2, seed=3)
     want = run_experts(args)
