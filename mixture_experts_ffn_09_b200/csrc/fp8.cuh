@@ -36,6 +36,24 @@ __device__ __forceinline__ float fp8_quotient(float u, float largest_u, float re
   return fmaf(fmaf(-q, largest_u, a), reciprocal, q);
 }
 
+// The same for values of any size: v times `by` over `top` is v / scale, as the
+// quotient by the largest magnitude where that is far from fp32's ends, else by
+// the scale itself.  (An infinite scale gives NaN for every value.)
+struct Fp8Divisor {
+  float by, top, reciprocal;
+  __device__ __forceinline__ Fp8Divisor(float amax, float scale) {
+    const bool direct = fp8_direct(amax);
+    by = direct ? kFp8Max : 1.f;
+    top = direct ? amax : scale;
+    reciprocal = 1.f / top;
+  }
+  __device__ __forceinline__ float operator()(float v) const {
+    const float a = v * by;
+    const float q = a * reciprocal;
+    return fmaf(fmaf(-q, top, a), reciprocal, q);
+  }
+};
+
 // Two values to packed e4m3 (the first in the low byte), nearest even,
 // saturating at +-448.
 __device__ __forceinline__ uint16_t fp8_pack2(float lo, float hi) {

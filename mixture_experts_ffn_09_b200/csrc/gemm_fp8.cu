@@ -538,11 +538,12 @@ __device__ __forceinline__ void finish_row(const Params& p, const Tile& tl, int 
     h.y = in ? silu_bf16_epilogue(v0.y) * v1.y : 0.f;
     h.z = in ? silu_bf16_epilogue(v0.z) * v1.z : 0.f;
     h.w = in ? silu_bf16_epilogue(v0.w) * v1.w : 0.f;
-    const float s = fp8_scale(warp_max(fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)))));
-    const float inv = 1.f / s;
+    const float m = warp_max(fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w))));
+    const float s = fp8_scale(m);
+    const Fp8Divisor over(m, s);
     if (in)
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + grow + col) =
-          fp8_pack4(h.x * inv, h.y * inv, h.z * inv, h.w * inv);
+          fp8_pack4(over(h.x), over(h.y), over(h.z), over(h.w));
     if (lane == 0) p.out_scales[static_cast<size_t>(tl.row0 + r) * ((p.n_out + 127) / 128) + tl.n_blk] = s;
   } else {
 #pragma unroll
@@ -1088,7 +1089,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (live) {
           m = fmaxf(st->amax[parity][0][r], st->amax[parity][1][r]);
           const float s = fp8_scale(m);
-          const float inv = 1.f / s;
+          const Fp8Divisor over(m, s);
           uint4 w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -1096,7 +1097,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float2 f = unpack(acc[0][8 * c + 2 * q]), g2 = unpack(acc[0][8 * c + 2 * q + 1]);
-              x[q] = fp8_pack4(f.x * inv, f.y * inv, g2.x * inv, g2.y * inv);
+              x[q] = fp8_pack4(over(f.x), over(f.y), over(g2.x), over(g2.y));
             }
             w[c] = make_uint4(x[0], x[1], x[2], x[3]);
           }

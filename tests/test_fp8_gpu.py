@@ -534,6 +534,32 @@ def test_experts_infinite_column(T):
     assert ((rest / want - 1).abs() <= 2.0 ** -4 + 2.0 ** -7).all()
 
 
+@pytest.mark.parametrize("T", [3, 300, 1000])       # 32-row tiles, 128-row tiles, pairs of CTAs
+def test_experts_round_ties_of_the_intermediate_to_even(T):
+    """h / scale halfway between two e4m3 values, in blocks whose scale's rounded reciprocal would end above the tie."""
+    r = torch.arange(1, 4096, 2, dtype=torch.float32)
+    above = (48 * r) * (1 / ((64 * r) / 448)) > 336             # 336 of 448 lies halfway between 320 and 352
+    r = r[above][:40]
+    D, F, n = 128, 40 * 128, len(r)
+    assert n == 40
+    x = torch.zeros(T, D, device="cuda")
+    x[:, 0] = 1.0
+    gu = torch.zeros(1, 2, F, D, device="cuda")
+    gu[0, 0, :, 0] = 64.0                                       # silu(64) = 64 in fp32
+    gu[0, 1, :, 0] = 0.75                                       # h = 48 r,
+    gu[0, 1, ::128, 0] = 1.0                                    # and once in each block 64 r, the largest
+    gus = torch.ones(1, 2, n, 1, device="cuda")
+    gus[0, 1, :, 0] = r.cuda()
+    dn = torch.zeros(1, D, F, device="cuda")
+    d = torch.arange(D, device="cuda")
+    dn[0, d, 128 * (d % n) + 1 + d // n] = 1.0
+    out = run_experts([x.to(F8), torch.ones(T, 1, device="cuda"), torch.zeros(T, 1, dtype=torch.int64, device="cuda"),
+                       torch.ones(T, 1, device="cuda"), gu.view(1, 2 * F, D).to(F8), gus, dn.to(F8),
+                       torch.ones(1, 1, n, device="cuda")])
+    want = 320 / 448 * 64 * r.cuda().double()[d % n]            # to even
+    assert ((out.double() / want - 1).abs() <= 2.0 ** -8 + 2.0 ** -11 + 4 * U32).all()     # bf16, fp16, the scale
+
+
 def test_experts_streams_graph_and_shared_workspace():
     """Another stream; two captured calls that share a workspace, replayed with new inputs."""
     args, other = make_experts(24, 256, 384, 8, 2, seed=1), make_experts(300, 256, 384, 8, 2, seed=2)
