@@ -694,7 +694,9 @@ def test_block_in_two_threads():
         st = torch.cuda.Stream()
         wrong = 0
         for _ in range(100):
-            wrong += not torch.equal(blk(xs[i], xs[i], stream=st), want[i])
+            got = blk(xs[i], xs[i], stream=st)
+            st.synchronize()                     # the comparison runs on the default stream
+            wrong += not torch.equal(got, want[i])
         bad[i] = wrong
 
     threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
