@@ -812,6 +812,9 @@ class MoEBlockFP8:
         quantize_fp8(gate_up_proj.view(E, 2, F, D), self.gate_up_proj.view(E, 2, F, D),
                      self.gate_up_scales, QUANT_BLOCK)
         quantize_fp8(down_proj, self.down_proj, self.down_scales, QUANT_BLOCK)
+        # calls may come on any stream: the weights are in place on return
+        if gate_up_proj.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
         self.residual_ = self.router_logits_ = self.selected_experts_ = self.routing_weights_ = None
 
     @property

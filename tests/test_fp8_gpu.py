@@ -682,6 +682,20 @@ def test_block_on_streams_at_once():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_block_is_ready_when_made():
+    """Its weights are in place on return, so that a first call on another stream needs no wait."""
+    make_block()                                 # kernels are loaded by their first launch, which waits for the device
+    a = randn(8192, 8192, seed=1)
+    for _ in range(30):
+        a @ a                                    # some 500 ms for the quantiser to queue behind
+    blk = make_block()
+    assert torch.cuda.current_stream().query()
+    x = randn(40, 256, seed=2).bfloat16()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    assert torch.equal(blk(x, x, stream=s), blk(x, x))
+
+
 def test_block_in_two_threads():
     """One block, two threads with a stream and tokens of their own, as many of them in each."""
     blk = make_block()
