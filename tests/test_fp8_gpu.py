@@ -293,6 +293,23 @@ def test_route_groups():
         assert torch.equal(sel, want)
 
 
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("o", [dict(), dict(scale=2.5), dict(score="sigmoid"), dict(score="sigmoid", scale=0.5, groups=4,
+                               top_groups=2, group_score="top2")], ids=str)
+@pytest.mark.parametrize("dtype,T,D,E", [(torch.bfloat16, 300, 264, 64), (torch.float32, 37, 33, 20)], ids=str)
+def test_route_groups_weights(dtype, T, D, E, o, norm):
+    """What route_groups writes is what select_experts makes of its logits, and right against 64 bits."""
+    x, r = randn(T, D, seed=1).to(dtype), randn(E, D, seed=2, std=0.1).to(dtype)
+    for bias in (None, randn(E, seed=4)):
+        lg = torch.empty(T, E, device="cuda")
+        sel, w = torch.empty(T, 5, dtype=torch.int64, device="cuda"), torch.empty(T, 5, device="cuda")
+        moe.route_groups(x, r, 5, norm, lg, sel, w, selection_bias=bias, **o)
+        s2, w2 = torch.empty_like(sel), torch.empty_like(w)
+        moe.select_experts(lg, 5, norm, s2, w2, selection_bias=bias, **o)
+        assert torch.equal(sel, s2) and torch.equal(w, w2)
+        check_select(lg, 5, norm, selection_bias=bias, **o)
+
+
 # ------------------------------------------------------------------ product
 def check_product(E, M, N, K, offsets, dtype=torch.bfloat16, seed=0):
     a, sa = rows8(M, K, seed)
@@ -558,6 +575,50 @@ def test_experts_round_ties_of_the_intermediate_to_even(T):
                        torch.ones(1, 1, n, device="cuda")])
     want = 320 / 448 * 64 * r.cuda().double()[d % n]            # to even
     assert ((out.double() / want - 1).abs() <= 2.0 ** -8 + 2.0 ** -11 + 4 * U32).all()     # bf16, fp16, the scale
+
+
+@pytest.mark.parametrize("cancel", [False, True])
+@pytest.mark.parametrize("T,D,F,E", [(3, 512, 256, 2), (40, 1024, 1152, 8),            # 32-row tiles, K blocks over a cluster or not
+                                     (700, 1088, 384, 4), (2000, 512, 256, 2)])        # 128-row tiles, pairs of CTAs
+def test_experts_outputs_are_kept_to_fp16(T, D, F, E, cancel):
+    """An intermediate that 8 bits hold exactly, so that only each expert's fp16 and the sum's bf16 are left: column
+    blocks far apart in size, and experts that cancel, where bf16 for each expert's output would be 8 times as far off."""
+    K = 2
+    up = (randn(E, F, D, seed=1) * 100).clamp(-448, 448).to(F8)
+    up.view(torch.uint8)[:, ::128] = 0x7E        # 448 in every block: the scale is a power of two
+    gu = torch.stack([torch.full_like(up, 64.0, dtype=torch.float32).to(F8), up], 1).view(E, 2 * F, D)     # silu(64) = 64
+    gus = torch.ones(E, 2, R.nblk(F), R.nblk(D), device="cuda")
+    size = torch.where(torch.arange(D, device="cuda") // 64 % 2 == 0, 2.0 ** 6, 2.0 ** -5)     # 2^11 apart
+    dn = (randn(E, D, F, seed=2) * size[:, None]).clamp(-448, 448).to(F8)
+    dns = torch.exp2(torch.randint(-12, 12, (E, R.nblk(D), R.nblk(F)), generator=gen(3), device="cuda").float())
+    sel = torch.rand(T, E, generator=gen(4), device="cuda").topk(K, 1).indices
+    w = torch.rand(T, K, generator=gen(5), device="cuda") + 0.1
+    if cancel:
+        less = randn(E // 2, D, F, seed=6) > 2
+        dn[1::2] = torch.where(less, torch.zeros((), device="cuda"), -dn[::2].float()).to(F8)
+        dns[1::2] = dns[::2]
+        sel = sel[:, :1] // 2 * 2 + torch.tensor([0, 1], device="cuda")
+        w = w[:, :1].expand(T, K).contiguous()
+    at = torch.arange(T, device="cuda") % D
+    x = torch.zeros(T, D, device="cuda")
+    x[torch.arange(T, device="cuda"), at] = 1.0
+    out = run_experts([x.to(F8), torch.ones(T, R.nblk(D), device="cuda"), sel, w, gu, gus, dn, dns]).double()
+    W = R.wide(dn, dns, R.BLOCK)
+    want, tol, coarse = (torch.zeros(T, D, dtype=torch.float64, device="cuda") for _ in range(3))
+    for e in range(E):
+        t, k = (sel == e).nonzero(as_tuple=True)
+        h = 64 * up[e].double()[:, at[t]].T
+        y, S, we = h @ W[e].T, h.abs() @ W[e].abs().T, w[t, k].double()[:, None]
+        cap = torch.nn.functional.pad(y.abs(), (0, -D % 64)).unflatten(1, (-1, 64)).amax(-1).repeat_interleave(64, 1)[:, :D]
+        want.index_add_(0, t, we * y)
+        coarse.index_add_(0, t, we * y.bfloat16().double())
+        # fp16: half a step of 2^-10 (of 2^-24 below 2^-14, with the block's largest at 2^14); the products' sums
+        # as in check_product; the weighted sum's K products and additions
+        tol.index_add_(0, t, we * (y.abs() * (2.0 ** -11 + 4 * U32) + cap * 2.0 ** -39 + S * (128 + R.nblk(F) + 4) * 2 * U32))
+    tol += (want.abs() + tol) * 2.0 ** -8
+    assert ((out - want).abs() <= tol).all()
+    if cancel:                                   # bf16 outputs would be seen
+        assert ((coarse - want).abs() > tol).double().mean() > 0.02
 
 
 def test_experts_streams_graph_and_shared_workspace():
