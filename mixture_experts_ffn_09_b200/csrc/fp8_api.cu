@@ -42,11 +42,14 @@ __global__ void __launch_bounds__(256) count_selected_kernel(const int64_t* __re
 // slot's rank is that within its warp (match), behind the earlier warps'
 // counts and the earlier slots' rows.  One launch instead of three (counts,
 // scan, scatter) for batches that the gate_up GEMM does not sort itself: 12 -> 4
-// us, measured with 192 slots of 64 experts.  A whole call against the other path:
-// 64 experts, 2040 slots 33 | 35 us, 3072 35.4 | 35.8, 4080 39.6 | 37.5; 256
-// experts, 4096 slots 54 | 66.
+// us, measured with 192 slots of 64 experts.  The other path's start costs more
+// the more experts there are, this one's turns with the slots.  A whole call
+// (widths of 128) against the other path, us: 8 experts, 2000 slots 24.3 | 24.6,
+// 2400 28.0 | 27.5; 32 experts, 2000 25.9 | 26.7, 2600 27.9 | 27.3; 64 experts,
+// 3000 29.4 | 29.7, 3400 30.7 | 29.9; 128 experts, 4096 34.5 | 36.5; 256 experts,
+// 4096 37.8 | 48.9.
 constexpr int kSmallThreads = 1024;
-constexpr int kSmallSlots = 4096;
+bool permute_in_one_cta(int64_t slots, int E) { return slots <= 1800 + 20LL * E && slots <= 4096; }
 
 __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(const int64_t* __restrict__ selected,
                                                                       int slots, int E,
@@ -463,7 +466,7 @@ moe_status_t moe_experts_forward_fp8(const void* x_fp8, const float* x_scales,
   StageScope scope(s);
   scope.begin();
   const bool sorts = gemm_fp8_sorts(R, L.gather);     // in the gate_up GEMM
-  if (!sorts && R <= kSmallSlots) {
+  if (!sorts && permute_in_one_cta(R, E)) {
     st = launched(launch_k(permute_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, false, 1,
                            selected_experts, R, E, offsets, perm, pos),
                   s, "permutation");

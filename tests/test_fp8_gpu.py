@@ -494,6 +494,17 @@ def test_experts_row_forms(T, D, F, E, K):
     assert (run_experts(args)[::7] == 0).all()
 
 
+@pytest.mark.parametrize("slots", [0, 2])           # the last sorted by one CTA, and the first that is not
+@pytest.mark.parametrize("E", [4, 8, 64, 128, 256])
+def test_experts_permutations(E, slots):
+    """1800 + 20 E slots, 4096 at most; unevenly filled, some unused."""
+    T = (min(1800 + 20 * E, 4096) + slots) // 2
+    args = make_experts(T, 128, 128, E, 2, seed=30)
+    args[2][: T // 2, 0] = 1
+    args[2][::5, 1] = -1
+    check_experts(args, run_experts(args))
+
+
 def test_experts_at_once():
     """Two calls on two streams at the same time, a workspace each."""
     args = [make_experts(24, 512, 384, 8, 2, seed=1), make_experts(300, 256, 384, 8, 2, seed=2)]
