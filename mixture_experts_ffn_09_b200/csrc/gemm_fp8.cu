@@ -1348,7 +1348,10 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& g, cudaStream_t s) {
   // 244, pair 257 (half a pair tile of padding per expert); 8192 rows of 4096 x
   // 14336: one CTA 470, pair 435.  Where even tiles of 32 rows leave half the
   // SMs idle, that form shares each one out: 64 rows of 4096 x 4096: 14 | 21 | 21,
-  // 128 rows: 19 | 22 | 22, 2000 rows of 256 x 7168: 19 | 31 | 32.
+  // 128 rows: 19 | 22 | 22, 2000 rows of 256 x 7168: 19 | 31 | 32.  The offsets
+  // are device data, so experts that differ cannot be told from even ones; 64
+  // experts of 1408 x 2048, 1500 rows, even: 36 | 39 | 57, 1400 of them one
+  // expert's: 48 | 40 | 56; 60000 rows, 40000 of them one expert's: 624 | 254 | 256.
   const long long few_tiles = tile_bound(g.M, g.E, Cfg<kFew>::TILE_M, gated ? blocks : (g.N + 255) / 256);
   int mode = g.M >= 768LL * g.E ? kPair : kOne;
   if (g.M <= 24LL * g.E || few_tiles * 2 <= num_sms()) mode = kFew;
