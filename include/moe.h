@@ -274,10 +274,11 @@ MOE_API moe_status_t moe_ffn_forward_noalloc(const void* x, const void* router,
  * one per 128 x 128 block: (ceil(rows / 128), ceil(cols / 128)) per matrix;
  * ragged last blocks are shorter.  The gate and the up half of a gate_up
  * weight (E, 2F, D) are blocked apart: its scales are
- * (E, 2, ceil(F / 128), ceil(D / 128)).  Any finite scales may be given; the
- * functions that write the format use max(|v|, 2^-100) / 448 and round to
- * nearest even.  A NaN stays a NaN; every value of a block that holds an
- * infinity reads back as NaN.
+ * (E, 2, ceil(F / 128), ceil(D / 128)).  Any finite scales may be given, as
+ * long as a row's times a weight block's stays within fp32's normal range (the
+ * products multiply the two first) or is 0; the functions that write the format
+ * use max(|v|, 2^-100) / 448 and round to nearest even.  A NaN stays a NaN;
+ * every value of a block that holds an infinity reads back as NaN.
  *
  * All calls below work like moe_ffn_forward: 16-byte aligned device pointers
  * (offsets: 4 bytes) on the current device, contiguous rows, asynchronous on
@@ -299,7 +300,9 @@ MOE_API moe_status_t moe_ffn_forward_noalloc(const void* x, const void* router,
  * residual, sum_out, out, and the pair out_fp8 and scales may be NULL; one of
  * out and out_fp8 is required.  sum_out and out may be x or residual
  * themselves (in place), but not each other; no other overlap is allowed.
- * h^2 is summed in fp32: a row whose sum passes its range gives zeros.
+ * h^2 is summed in fp32: a row whose sum passes its range gives zeros, and
+ * squares below it count as 0 (values under 1e-19; with eps = 0 a row of them
+ * is not normed to 1).
  * Any D up to MOE_NORM_MAX_D (vector loads when D is a multiple of 8).
  */
 #define MOE_NORM_MAX_D 32768

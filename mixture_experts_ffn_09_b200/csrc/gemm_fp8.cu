@@ -26,9 +26,11 @@
 //          that four warps read a block, a half and a weight block each, and
 //          no longer take longer than its MMAs (16 rows of 4096 x 14336: 20.7
 //          -> 18.7 us).
-// 8192 rows of 4096 x 14336 (kPair): 440 us, 2.19 PFLOP/s, at the board's power
-// limit (1.4 to 1.5 GHz).  9973 rows over 64 experts of 1408 x 2048, unevenly
-// (kOne): 60 us.  16 rows of 4096 x 14336 (kFew): 19 us, the weights at 3.1 TB/s.
+// 8192 rows of 4096 x 14336 (kPair): 435 us in short runs, 2.21 PFLOP/s at 1.45
+// GHz with the tensor pipe active in 64% of cycles; 500 us in runs of seconds,
+// at the board's power limit.  9973 rows over 64 experts of 1408 x 2048,
+// unevenly (kOne): 60 us, 70 in runs of seconds.  16 rows of 4096 x 14336 (kFew):
+// 19 us, the weights at 3.1 TB/s.
 //
 // One persistent CTA per SM (or pair of CTAs per two SMs), 384 threads:
 //   warp 0      TMA producer: A rows x 128 columns and B rows (256, or this CTA's

@@ -14,7 +14,7 @@
 // experts the logits alone would take 3 us), so what ranks experts is computed
 // with the fast exponential and reciprocal, and only the K chosen scores are
 // computed again with expf and a division.  16384 tokens, 256 experts, 8 of
-// them from 4 of 8 groups: 25 us, some 900 instructions a token (50 us with
+// them from 4 of 8 groups: 25 us, some 920 instructions a token (50 us with
 // expf and a division for all, a scan for each choice and an fp64 path of
 // 25000 cycles).
 //

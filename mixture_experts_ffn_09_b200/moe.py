@@ -782,7 +782,8 @@ class MoEBlockFP8:
     quantises once: router (E, D) stays in its type, gate_up_proj (E, 2F, D)
     and down_proj (E, D, F) become e4m3 with block scales.  With norm_weight
     (D,) the input is normed first; ``forward(x, residual)`` then returns the
-    block's output, and ``residual_`` holds x + residual.  Routing options are
+    block's output, and ``residual_`` holds x + residual.  The output is bf16,
+    whatever the type of x (bf16 or float32, the router's).  Routing options are
     those of :func:`select_experts`.  Keeps ``router_logits_``,
     ``selected_experts_`` and ``routing_weights_`` of the last call.
 
